@@ -7,15 +7,17 @@ has not been built, every call raises ``MuonLibraryMissing``; there is no fallba
 Entry points mirror ``include/muon.h``: :func:`workspace_size`, :func:`muon_step`,
 :func:`adamw_step`, :func:`step_cost`, :func:`plan_describe`, :func:`profile_begin`,
 :func:`profile_end`, :func:`strerror`, :func:`last_error`, :func:`version`,
-:func:`shutdown`; and ``include/shampoo.h``: :func:`shampoo_workspace_size`,
-:func:`shampoo_step` (:class:`ShampooStep`), :func:`shampoo_plan_describe`.
+:func:`shutdown`; ``include/shampoo.h``: :func:`shampoo_workspace_size`,
+:func:`shampoo_step` (:class:`ShampooStep`), :func:`shampoo_plan_describe`; and
+``include/muon_grad.h``: :func:`grad_norm`, :func:`grad_clip`, :func:`clip_grad_norm`
+(:class:`GradClip`), :func:`adamw_list_step` (:class:`AdamWStep`).
 """
 
 from __future__ import annotations
 
 import ctypes
 import json
-from ctypes import POINTER, c_char, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().with_name("libmuon.so")
@@ -77,6 +79,28 @@ class shampoo_hparams(ctypes.Structure):
     _fields_ = [("lr", c_float), ("beta2", c_float), ("eps", c_float), ("root_iters", c_int32)]
 
 
+class muon_grad(ctypes.Structure):
+    _fields_ = [("grad", c_void_p), ("n", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
+class adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", c_void_p), ("grad", c_void_p), ("m", c_void_p), ("v", c_void_p), ("master", c_void_p),
+                ("n", c_int64), ("param_dtype", c_int32), ("grad_dtype", c_int32), ("decay", c_float),
+                ("reserved", c_int32)]
+
+
+class muon_grad_list(ctypes.Structure):
+    _fields_ = [("opaque", c_uint64 * 8)]
+
+
+class adamw_list(ctypes.Structure):
+    _fields_ = [("opaque", c_uint64 * 8)]
+
+
+class muon_clip(ctypes.Structure):
+    _fields_ = [("norm", c_void_p), ("max_norm", c_float), ("reserved", c_int32)]
+
+
 _MATP = POINTER(muon_matrix)
 _HPP = POINTER(muon_hparams)
 _SMATP = POINTER(shampoo_matrix)
@@ -114,6 +138,14 @@ _SIGNATURES = {
     "shampoo_workspace_size": (c_int, [_SMATP, c_int32, _SHPP, POINTER(c_size_t)]),
     "shampoo_step": (c_int, [_SMATP, c_int32, _SHPP, c_void_p, c_size_t, c_void_p]),
     "shampoo_plan_describe": (c_int, [_SMATP, c_int32, _SHPP, c_char_p, c_size_t]),
+    "muon_grad_list_size": (c_int, [POINTER(muon_grad), c_int32, POINTER(c_size_t)]),
+    "muon_grad_list_init": (c_int, [POINTER(muon_grad), c_int32, c_void_p, c_size_t, c_void_p, POINTER(muon_grad_list)]),
+    "muon_grad_norm": (c_int, [POINTER(muon_grad_list), c_int32, c_void_p, c_void_p]),
+    "muon_grad_clip": (c_int, [POINTER(muon_grad_list), POINTER(muon_clip), c_void_p]),
+    "muon_grad_clip_norm": (c_int, [POINTER(muon_grad_list), c_int32, c_float, c_void_p, c_void_p]),
+    "adamw_list_size": (c_int, [POINTER(adamw_tensor), c_int32, POINTER(c_size_t)]),
+    "adamw_list_init": (c_int, [POINTER(adamw_tensor), c_int32, c_void_p, c_size_t, c_void_p, POINTER(adamw_list)]),
+    "adamw_list_step": (c_int, [POINTER(adamw_list), POINTER(adamw_hparams), POINTER(muon_clip), c_void_p]),
 }
 
 _lib = None
@@ -557,12 +589,12 @@ def profile_begin() -> None:
 
 def profile_end() -> dict:
     """Stop per-launch timing and return {kernel: {launches, ms, flops, bytes}}."""
-    out = (muon_kernel_stat * 16)()
+    out = (muon_kernel_stat * 32)()
     n = c_int32(0)
-    _check(lib().muon_profile_end(out, 16, ctypes.byref(n)))
+    _check(lib().muon_profile_end(out, 32, ctypes.byref(n)))
     return {out[i].name.decode(): {"launches": out[i].launches, "ms": out[i].ms,
                                    "flops": out[i].flops, "bytes": out[i].bytes}
-            for i in range(min(n.value, 16))}
+            for i in range(min(n.value, 32))}
 
 
 # --- Shampoo (include/shampoo.h) --------------------------------------------------------
@@ -678,3 +710,220 @@ def shampoo_step(params, grads, lefts, rights, *, stream=None, **hp) -> None:
     with torch.cuda.stream(s):
         step = ShampooStep(params, grads, lefts, rights, **hp)
     step(s)
+
+
+# --- lists of tensors (include/muon_grad.h) ---------------------------------------------
+
+NORM_KINDS = {"l2": 0, "inf": 1}
+
+
+def _norm_kind(kind) -> int:
+    code = NORM_KINDS.get(kind)
+    if code is None:
+        raise ValueError(f"unknown kind of norm {kind!r} ('l2' or 'inf')")
+    return code
+
+
+def _list_device(tensors, device=None):
+    """The one GPU that all tensors of a list are on (an empty list: `device`, or the current
+    one)."""
+    import torch
+
+    devices = {t.device for t in tensors}
+    if device is not None:
+        device = torch.device(device)
+        devices.add(torch.device("cuda", torch.cuda.current_device()) if device.type == "cuda" and
+                    device.index is None else device)
+    if not devices:
+        return torch.device("cuda", torch.cuda.current_device())
+    if len(devices) > 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"the tensors of a list must be on one GPU, not on {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def grad_array(grads):
+    """Pack a list of contiguous device tensors (any shape, bfloat16 or float32) into a ctypes
+    muon_grad array."""
+    arr = (muon_grad * max(1, len(grads)))()
+    for i, g in enumerate(grads):
+        if not g.is_contiguous():
+            raise ValueError(f"tensor {i}: gradients must be contiguous")
+        arr[i] = muon_grad(g.data_ptr(), g.numel(), _dtype_code(g), 0)
+    return arr
+
+
+def adamw_array(params, grads, ms, vs, masters=None, decays=None):
+    """Pack lists of device tensors into a ctypes adamw_tensor array: param (bfloat16 or
+    float32), grad (bfloat16 or float32), m and v (float32), a float32 master or None for each
+    param (a list, or None for none at all) and the factor on each tensor's weight decay (a
+    list, or None for 1)."""
+    import torch
+
+    n = len(params)
+    masters = [None] * n if masters is None else list(masters)
+    decays = [1.0] * n if decays is None else list(decays)
+    if not (n == len(grads) == len(ms) == len(vs) == len(masters) == len(decays)):
+        raise ValueError("params, grads, ms, vs, masters and decays must have the same length")
+    arr = (adamw_tensor * max(1, n))()
+    for i, (p, g, m, v, w, d) in enumerate(zip(params, grads, ms, vs, masters, decays)):
+        for name, t in (("param", p), ("grad", g), ("m", m), ("v", v), ("master", w)):
+            if t is None and name == "master":
+                continue
+            if not t.is_contiguous() or t.shape != p.shape:
+                raise ValueError(f"tensor {i}: {name} must be contiguous and of the param's shape {tuple(p.shape)}")
+            if name in ("m", "v", "master") and t.dtype != torch.float32:
+                raise TypeError(f"tensor {i}: {name} must be float32")
+        arr[i] = adamw_tensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                              0 if w is None else w.data_ptr(), p.numel(), _dtype_code(p), _dtype_code(g),
+                              float(d), 0)
+    return arr
+
+
+class _List:
+    """A list of tensors laid out on one device: what GradClip and AdamWStep share."""
+
+    _kind = None  # name of the C list type
+
+    def _lay_out(self, arr, count, tensors, device, workspace, stream):
+        import torch
+
+        self.count = count
+        self.device = _list_device(tensors, device)
+        size = c_size_t(0)
+        _check(getattr(lib(), f"{self._kind}_size")(arr, count, ctypes.byref(size)))
+        self.ws_bytes = int(size.value)
+        home = self._stream(stream)
+        self._home = home.cuda_stream
+        with torch.cuda.device(self.device), torch.cuda.stream(home):
+            if workspace is None:
+                workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
+            if workspace.numel() < self.ws_bytes:
+                raise ValueError(f"workspace has {workspace.numel()} bytes, needs {self.ws_bytes}")
+            self.workspace = workspace
+            self.list = (muon_grad_list if self._kind == "muon_grad_list" else adamw_list)()
+            _check(getattr(lib(), f"{self._kind}_init")(arr, count, c_void_p(workspace.data_ptr()), workspace.numel(),
+                                                        c_void_p(self._home), ctypes.byref(self.list)))
+        self._list = ctypes.byref(self.list)
+
+    def _stream(self, stream):
+        import torch
+
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
+
+    def _call(self, fn, args, stream):
+        """fn(list, *args, stream) on the list's device."""
+        import torch
+
+        s = self._stream(stream)
+        if s.cuda_stream != self._home:
+            # The allocator keeps the workspace until this stream, too, has passed the call.
+            self.workspace.record_stream(s)
+        if torch.cuda.current_device() == self.device.index:
+            _check(fn(self._list, *args, c_void_p(s.cuda_stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn(self._list, *args, c_void_p(s.cuda_stream)))
+
+    def _norm_arg(self, norm):
+        import torch
+
+        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.device:
+            raise ValueError(f"norm must be one float32 value on {self.device}")
+        return c_void_p(norm.data_ptr())
+
+    def _clip_arg(self, clip):
+        norm, max_norm = clip
+        return ctypes.byref(muon_clip(self._norm_arg(norm), float(max_norm), 0))
+
+
+class GradClip(_List):
+    """A list of gradients laid out once, for their global norm and clipping by it.
+
+    The tensors must stay where they are as long as this is used (their values may change):
+    after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
+    `stream` (default: the current one) at construction; a use on another stream must come
+    after it.  Two calls in flight at once need two of these."""
+
+    _kind = "muon_grad_list"
+
+    def __init__(self, grads, *, device=None, workspace=None, stream=None):
+        self.grads = list(grads)
+        self._lay_out(grad_array(self.grads), len(self.grads), self.grads, device, workspace, stream)
+
+    def _out(self, out, stream):
+        import torch
+
+        if out is not None:
+            return out
+        with torch.cuda.stream(None if stream is None else self._stream(stream)):
+            return torch.empty((), dtype=torch.float32, device=self.device)
+
+    def norm(self, kind="l2", *, out=None, stream=None):
+        """The norm of all gradients, as a float32 device tensor (`out`, or a new one that
+        belongs to the stream of the call)."""
+        code = _norm_kind(kind)
+        out = self._out(out, stream)
+        self._call(lib().muon_grad_norm, (code, self._norm_arg(out)), stream)
+        return out
+
+    def clip(self, norm, max_norm, *, stream=None) -> None:
+        """Scale the gradients in place by min(1, max_norm / (norm + 1e-6)); `norm` is a float32
+        device tensor, for example one that was reduced over ranks."""
+        self._call(lib().muon_grad_clip, (self._clip_arg((norm, max_norm)),), stream)
+
+    def clip_norm(self, max_norm, kind="l2", *, out=None, stream=None):
+        """norm(), then clip() by it; returns the norm from before."""
+        code = _norm_kind(kind)
+        out = self._out(out, stream)
+        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), self._norm_arg(out)), stream)
+        return out
+
+
+class AdamWStep(_List):
+    """AdamW over fixed lists of device tensors, laid out once (see adamw_array for the lists).
+
+    Each call enqueues one ``adamw_list_step`` on the current (or given) stream.  As with
+    GradClip, the tensors stay where they are and the layout goes to `stream`."""
+
+    _kind = "adamw_list"
+
+    def __init__(self, params, grads, ms, vs, *, masters=None, decays=None, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8,
+                 weight_decay=0.1, device=None, workspace=None, stream=None):
+        self.params, self.grads, self.ms, self.vs = list(params), list(grads), list(ms), list(vs)
+        self.masters = None if masters is None else list(masters)
+        self.hp = adamw_hparams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 1)
+        arr = adamw_array(self.params, self.grads, self.ms, self.vs, self.masters, decays)
+        tensors = self.params + self.grads + self.ms + self.vs + [w for w in self.masters or [] if w is not None]
+        self._lay_out(arr, len(self.params), tensors, device, workspace, stream)
+
+    def __call__(self, step, *, lr=None, clip=None, stream=None) -> None:
+        """Update number `step` (>= 1), with `lr` from now on if given; clip = (norm, max_norm)
+        scales the gradients by min(1, max_norm / (norm + 1e-6)) as they are read."""
+        self.hp.step = int(step)
+        if lr is not None:
+            self.hp.lr = float(lr)
+        arg = None if clip is None else self._clip_arg(clip)
+        self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream)
+
+
+def grad_norm(grads, kind="l2", *, device=None, stream=None):
+    """The global norm of a list of gradients (see GradClip.norm), laid out for this call."""
+    return GradClip(grads, device=device, stream=stream).norm(kind, stream=stream)
+
+
+def grad_clip(grads, norm, max_norm, *, device=None, stream=None) -> None:
+    """Scale a list of gradients in place by a norm in hand (see GradClip.clip)."""
+    GradClip(grads, device=device, stream=stream).clip(norm, max_norm, stream=stream)
+
+
+def clip_grad_norm(grads, max_norm, kind="l2", *, device=None, stream=None):
+    """Clip a list of gradients in place by their global norm, and return it (see
+    GradClip.clip_norm)."""
+    return GradClip(grads, device=device, stream=stream).clip_norm(max_norm, kind, stream=stream)
+
+
+def adamw_list_step(params, grads, ms, vs, *, step=1, clip=None, stream=None, **kw) -> None:
+    """One AdamW update of lists of tensors (see AdamWStep), laid out for this call."""
+    AdamWStep(params, grads, ms, vs, stream=stream, **kw)(step, clip=clip, stream=stream)

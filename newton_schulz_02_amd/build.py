@@ -24,8 +24,8 @@ BUILD = PKG / "_build"
 LIB = PKG / "libmuon.so"
 ARCH = "gfx950"
 
-SOURCES = ["planner.cpp", "shampoo_plan.cpp", "muon_api.cpp", "owner.cpp", "kernels_elementwise.hip", "kernels_gemm.hip",
-           "kernels_gemm_wide.hip", "noalloc.hip"]
+SOURCES = ["planner.cpp", "shampoo_plan.cpp", "list_plan.cpp", "muon_api.cpp", "owner.cpp", "kernels_elementwise.hip",
+           "kernels_list.hip", "kernels_gemm.hip", "kernels_gemm_wide.hip", "noalloc.hip"]
 # Sources compiled a second time with extra defines: (source, object stem, flags).
 VARIANTS = [("kernels_gemm.hip", "kernels_gemm_deep", ["-DMUON_GEMM_DEEP=1"]),
             ("kernels_gemm.hip", "kernels_gemm_small", ["-DMUON_GEMM_SMALL=1"])]

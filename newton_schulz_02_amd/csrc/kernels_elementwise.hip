@@ -11,6 +11,7 @@
 // summary, Methodology §1 (AdamW for the non-matrix tail).
 #include <hip/hip_runtime.h>
 
+#include "list_math.h"
 #include "muon_internal.h"
 
 using namespace muon;
@@ -203,14 +204,6 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a) {
     for (int i = threadIdx.x; i < a.split_cnt_n; i += 256) a.split_cnt[i] = 0;
 }
 
-__device__ __forceinline__ void adamw_one(float& p, float g, float& m, float& v, const AdamArgs& a) {
-  m = fmaf(a.beta1, m, (1.0f - a.beta1) * g);
-  v = fmaf(a.beta2, v, (1.0f - a.beta2) * g * g);
-  const float mh = m / a.bc1;
-  const float vh = v / a.bc2;
-  p = p - a.lr * (mh / (sqrtf(vh) + a.eps) + a.wd * p);
-}
-
 __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   const int64_t stride = int64_t(gridDim.x) * 256 * 4;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.p) | reinterpret_cast<uintptr_t>(a.g) |
@@ -221,17 +214,17 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       const float4 g = *reinterpret_cast<const float4*>(a.g + i);
       float4 m = *reinterpret_cast<const float4*>(a.m + i);
       float4 v = *reinterpret_cast<const float4*>(a.v + i);
-      adamw_one(p.x, g.x, m.x, v.x, a);
-      adamw_one(p.y, g.y, m.y, v.y, a);
-      adamw_one(p.z, g.z, m.z, v.z, a);
-      adamw_one(p.w, g.w, m.w, v.w, a);
+      adamw_one(p.x, g.x, m.x, v.x, a, a.wd);
+      adamw_one(p.y, g.y, m.y, v.y, a, a.wd);
+      adamw_one(p.z, g.z, m.z, v.z, a, a.wd);
+      adamw_one(p.w, g.w, m.w, v.w, a, a.wd);
       *reinterpret_cast<float4*>(a.p + i) = p;
       *reinterpret_cast<float4*>(a.m + i) = m;
       *reinterpret_cast<float4*>(a.v + i) = v;
     } else {
       for (int64_t j = i; j < i + 4 && j < a.n; ++j) {
         float p = a.p[j], m = a.m[j], v = a.v[j];
-        adamw_one(p, a.g[j], m, v, a);
+        adamw_one(p, a.g[j], m, v, a, a.wd);
         a.p[j] = p;
         a.m[j] = m;
         a.v[j] = v;

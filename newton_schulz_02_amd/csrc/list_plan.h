@@ -1,0 +1,54 @@
+// Host layout of the list operators (muon_grad.h): the descriptor table of a list of
+// tensors, cut into chunks, as the kernels of kernels_list.hip read it.
+//
+// A list's chunks are numbered through: tensor i owns the chunks [first_i, first_{i+1}), the
+// last of each tensor being partial.  Empty tensors have no entry.  Tables are written to the
+// caller's workspace once (the *_init calls) and only read afterwards:
+//   head (256 bytes: status word, the norm's ticket), entries, and for a gradient list the
+//   norm's partial results.
+#pragma once
+
+#include <cstdint>
+#include <string>
+#include <vector>
+
+#include "../../include/muon_grad.h"
+#include "muon_internal.h"
+
+namespace muon {
+
+constexpr int32_t kMaxList = 1 << 20;              // tensors in one list
+constexpr int64_t kMaxListElems = int64_t(1) << 40;  // elements in one list
+
+struct ListTable {
+  std::vector<uint32_t> words;  // head and entries, as uploaded
+  uint32_t chunks = 0;
+  int32_t entries = 0;          // tensors that are not empty
+  int64_t elems = 0;
+  double read_bytes = 0.0;      // gradients (all operands of an AdamW list) read once
+  double write_bytes = 0.0;     // outputs written once
+  size_t ws_bytes = 0;
+};
+
+// Validate a list and lay out its table.  MUON_OK, or a status with the reason in *err.
+int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::string* err);
+int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, std::string* err);
+
+// What a muon_grad_list / adamw_list holds.
+struct ListHandle {
+  uint64_t magic;     // kind of list
+  uint64_t workspace;
+  uint32_t chunks;
+  int32_t entries;
+  int32_t device;
+  int32_t reserved;
+  int64_t elems;
+  double read_bytes, write_bytes;
+  uint64_t check;     // over the fields above: an uninitialised or foreign handle is refused
+};
+constexpr uint64_t kGradListMagic = 0x6d756f6e67726164ull;
+constexpr uint64_t kAdamListMagic = 0x6d756f6e6164616dull;
+
+uint64_t handle_check(const ListHandle& h);
+
+}  // namespace muon

@@ -14,7 +14,9 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "../../include/muon_grad.h"
 #include "../../include/muon_test_hooks.h"
+#include "list_plan.h"
 #include "muon_internal.h"
 #include "planner.h"
 #include "shampoo_plan.h"
@@ -874,6 +876,254 @@ int adamw_step(float* p, const float* g, float* m, float* v, int64_t n, const ad
     if ((rc = current_device(&dev)) != MUON_OK) return rc;
     if ((rc = check_device(dev)) != MUON_OK) return rc;
     return timed(dev, s, "adamw", 0.0, 28.0 * double(n), [&] { return muon_launch_adamw(a, s); });
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+// --- list operators (muon_grad.h) ------------------------------------------------------------
+
+namespace {
+
+static_assert(sizeof(ListHandle) == sizeof(muon_grad_list) && sizeof(ListHandle) == sizeof(adamw_list),
+              "a laid-out list holds one handle");
+
+// Write a list's table to its workspace and fill its handle.
+int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t workspace_bytes, void* hip_stream,
+              void* list) {
+  if (!list) return fail(MUON_EINVAL, "list is NULL");
+  if (!workspace) return fail(MUON_EINVAL, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(MUON_EINVAL, "workspace is not 256-byte aligned");
+  if (workspace_bytes < t.ws_bytes)
+    return fail(MUON_ENOSPC, "workspace has " + std::to_string(workspace_bytes) + " bytes, needs " +
+                                 std::to_string(t.ws_bytes));
+  std::lock_guard<std::mutex> lock(g_mu);
+  ListHandle h;
+  std::memset(&h, 0, sizeof h);
+  int rc = MUON_OK, dev = 0;
+  if ((rc = current_device(&dev)) != MUON_OK) return rc;
+  if ((rc = check_device(dev)) != MUON_OK) return rc;
+  const int e = muon_put_words(workspace, t.words.data(), t.words.size() * 4, hip_stream);
+  if (e != hipSuccess) return hip_fail(hipError_t(e), "list layout (kernel arguments)");
+  h.magic = magic;
+  h.workspace = uint64_t(reinterpret_cast<uintptr_t>(workspace));
+  h.chunks = t.chunks;
+  h.entries = t.entries;
+  h.device = dev;
+  h.elems = t.elems;
+  h.read_bytes = t.read_bytes;
+  h.write_bytes = t.write_bytes;
+  h.check = handle_check(h);
+  std::memcpy(list, &h, sizeof h);
+  return MUON_OK;
+}
+
+// A handle that an init call filled.
+int open_list(const void* list, uint64_t magic, ListHandle* h) {
+  if (!list) return fail(MUON_EINVAL, "list is NULL");
+  std::memcpy(h, list, sizeof *h);
+  if (h->magic != magic || h->check != handle_check(*h))
+    return fail(MUON_EINVAL, "not a list that an init call of its kind laid out");
+  return MUON_OK;
+}
+
+// Caller holds g_mu.
+int on_list_device(const ListHandle& h, int* dev) {
+  int rc;
+  if ((rc = current_device(dev)) != MUON_OK) return rc;
+  if (*dev != h.device)
+    return fail(MUON_EINVAL, "the list was laid out on device " + std::to_string(h.device) + ", the current one is " +
+                                 std::to_string(*dev));
+  return check_device(*dev);
+}
+
+int check_max_norm(float max_norm) {
+  if (!std::isfinite(max_norm) || max_norm < 0.0f) return fail(MUON_EINVAL, "max_norm is not finite and >= 0");
+  return MUON_OK;
+}
+
+int check_norm(const float* norm) {
+  if (!norm) return fail(MUON_EINVAL, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(MUON_EINVAL, "norm is not 4-byte aligned");
+  return MUON_OK;
+}
+
+int check_clip(const muon_clip* clip) {
+  int rc;
+  if (!clip) return fail(MUON_EINVAL, "clip is NULL");
+  if (clip->reserved != 0) return fail(MUON_EINVAL, "clip: reserved field must be 0");
+  if ((rc = check_norm(clip->norm)) != MUON_OK) return rc;
+  return check_max_norm(clip->max_norm);
+}
+
+int check_kind(int32_t kind) {
+  if (kind != MUON_NORM_L2 && kind != MUON_NORM_INF) return fail(MUON_EINVAL, "unknown kind of norm");
+  return MUON_OK;
+}
+
+GradArgs grad_args(const ListHandle& h) {
+  GradArgs a;
+  std::memset(&a, 0, sizeof a);
+  char* ws = reinterpret_cast<char*>(uintptr_t(h.workspace));
+  a.recs = reinterpret_cast<const GradRec*>(ws + kListHead);
+  a.count = h.entries;
+  a.chunks = h.chunks;
+  a.parts = reinterpret_cast<double*>(ws + round_up(kListHead + int64_t(h.entries) * int64_t(sizeof(GradRec)), 256));
+  return a;
+}
+
+// Caller holds g_mu.
+int launch_norm(int dev, hipStream_t s, const ListHandle& h, int32_t kind, float* norm) {
+  GradArgs a = grad_args(h);
+  a.norm = norm;
+  a.inf = kind == MUON_NORM_INF;
+  return timed(dev, s, "grad_norm", 0.0, h.read_bytes, [&] { return muon_launch_grad_norm(a, s); });
+}
+int launch_clip(int dev, hipStream_t s, const ListHandle& h, const float* norm, float max_norm) {
+  GradArgs a = grad_args(h);
+  a.clip = {norm, max_norm};
+  return timed(dev, s, "grad_clip", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_grad_clip(a, s); });
+}
+
+int check_adamw(const adamw_hparams* hp) {
+  if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+  const float fs[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
+  for (float f : fs)
+    if (!std::isfinite(f)) return fail(MUON_EINVAL, "non-finite hyperparameter");
+  if (hp->step < 1) return fail(MUON_EINVAL, "step must be >= 1");
+  if (hp->beta1 < 0.0f || hp->beta1 >= 1.0f || hp->beta2 < 0.0f || hp->beta2 >= 1.0f)
+    return fail(MUON_EINVAL, "beta1/beta2 outside [0, 1)");
+  return MUON_OK;
+}
+
+}  // namespace
+
+int muon_grad_list_size(const muon_grad* grads, int32_t count, size_t* bytes) {
+  try {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    ListTable t;
+    std::string err;
+    const int rc = build_grad_list(grads, count, &t, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = t.ws_bytes;
+    return MUON_OK;
+  } catch (const std::exception& e) {
+    return fail(MUON_EINVAL, e.what());
+  }
+}
+
+int adamw_list_size(const adamw_tensor* tensors, int32_t count, size_t* bytes) {
+  try {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    ListTable t;
+    std::string err;
+    const int rc = build_adamw_list(tensors, count, &t, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = t.ws_bytes;
+    return MUON_OK;
+  } catch (const std::exception& e) {
+    return fail(MUON_EINVAL, e.what());
+  }
+}
+
+int muon_grad_list_init(const muon_grad* grads, int32_t count, void* workspace, size_t workspace_bytes,
+                        void* hip_stream, muon_grad_list* list) {
+  try {
+    ListTable t;
+    std::string err;
+    const int rc = build_grad_list(grads, count, &t, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    return init_list(t, kGradListMagic, workspace, workspace_bytes, hip_stream, list);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int adamw_list_init(const adamw_tensor* tensors, int32_t count, void* workspace, size_t workspace_bytes,
+                    void* hip_stream, adamw_list* list) {
+  try {
+    ListTable t;
+    std::string err;
+    const int rc = build_adamw_list(tensors, count, &t, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    return init_list(t, kAdamListMagic, workspace, workspace_bytes, hip_stream, list);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int muon_grad_norm(const muon_grad_list* list, int32_t kind, float* norm, void* hip_stream) {
+  try {
+    ListHandle h;
+    int rc, dev = 0;
+    if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
+    if ((rc = check_kind(kind)) != MUON_OK || (rc = check_norm(norm)) != MUON_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    return launch_norm(dev, s, h, kind, norm);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int muon_grad_clip(const muon_grad_list* list, const muon_clip* clip, void* hip_stream) {
+  try {
+    ListHandle h;
+    int rc, dev = 0;
+    if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
+    if ((rc = check_clip(clip)) != MUON_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    return launch_clip(dev, s, h, clip->norm, clip->max_norm);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm, float* norm, void* hip_stream) {
+  try {
+    ListHandle h;
+    int rc, dev = 0;
+    if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
+    if ((rc = check_kind(kind)) != MUON_OK || (rc = check_norm(norm)) != MUON_OK) return rc;
+    if ((rc = check_max_norm(max_norm)) != MUON_OK) return rc;
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    if ((rc = launch_norm(dev, s, h, kind, norm)) != MUON_OK) return rc;
+    return launch_clip(dev, s, h, norm, max_norm);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream) {
+  try {
+    ListHandle h;
+    int rc, dev = 0;
+    if ((rc = open_list(list, kAdamListMagic, &h)) != MUON_OK) return rc;
+    if ((rc = check_adamw(hp)) != MUON_OK) return rc;
+    if (clip && (rc = check_clip(clip)) != MUON_OK) return rc;
+    AdamListArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.recs = reinterpret_cast<const AdamRec*>(uintptr_t(h.workspace) + uintptr_t(kListHead));
+    a.count = h.entries;
+    a.chunks = h.chunks;
+    if (clip) a.clip = {clip->norm, clip->max_norm};
+    a.lr = hp->lr;
+    a.beta1 = hp->beta1;
+    a.beta2 = hp->beta2;
+    a.eps = hp->eps;
+    a.wd = hp->weight_decay;
+    a.bc1 = float(1.0 - std::pow(double(hp->beta1), double(hp->step)));
+    a.bc2 = float(1.0 - std::pow(double(hp->beta2), double(hp->step)));
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    return timed(dev, s, "adamw_list", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_adamw_list(a, s); });
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }

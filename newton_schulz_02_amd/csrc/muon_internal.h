@@ -175,6 +175,54 @@ struct AdamArgs {
   float bc1, bc2;        // 1 - beta1^t, 1 - beta2^t (computed on the host in double)
 };
 
+// List operators (list_plan.h, kernels_list.hip).
+constexpr int64_t kListHead = 256;    // head of a list's workspace; entries follow
+constexpr int64_t kGradChunk = 16384; // bytes of one chunk of a gradient list
+constexpr int64_t kAdamChunk = 2048;  // elements of one chunk of an AdamW list
+constexpr int kNormParts = 2048;      // most workgroups (and partial results) of a norm
+
+struct GradRec {
+  uint64_t ptr;
+  int64_t n;
+  uint32_t first;  // first chunk
+  uint32_t dtype;
+};
+
+struct AdamRec {
+  uint64_t param, grad, m, v, master;
+  int64_t n;
+  uint32_t first;  // first chunk
+  uint16_t param_bf16, grad_bf16;
+  float decay;
+  uint32_t reserved;
+};
+
+// Where a clip coefficient comes from; norm null: none (1).
+struct ClipArg {
+  const float* norm;
+  float max_norm;
+};
+
+struct GradArgs {
+  const GradRec* recs;
+  int32_t count;
+  uint32_t chunks;
+  double* parts;   // one per workgroup of the norm
+  int32_t nparts;
+  float* norm;     // output of the norm
+  int32_t inf;     // largest magnitude instead of L2
+  ClipArg clip;
+};
+
+struct AdamListArgs {
+  const AdamRec* recs;
+  int32_t count;
+  uint32_t chunks;
+  ClipArg clip;
+  float lr, beta1, beta2, eps, wd;
+  float bc1, bc2;
+};
+
 inline int64_t round_up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 inline int64_t ceil_div(int64_t x, int64_t q) { return (x + q - 1) / q; }
 
@@ -188,6 +236,9 @@ int muon_launch_gemm_deep(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_gemm_small(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_gemm_wide(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_adamw(const muon::AdamArgs& a, void* stream);
+int muon_launch_grad_norm(const muon::GradArgs& a, void* stream);
+int muon_launch_grad_clip(const muon::GradArgs& a, void* stream);
+int muon_launch_adamw_list(const muon::AdamListArgs& a, void* stream);
 // noalloc.hip: device address of the allocation-free entry point's scratch array on device
 // `dev` (asked of the runtime once per device; that device must be current), and a copy of
 // a small host block (bytes a multiple of 4) to device memory through kernel arguments.
