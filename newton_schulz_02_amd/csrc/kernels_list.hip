@@ -32,32 +32,101 @@ __device__ __forceinline__ int find(const Rec* recs, int count, uint32_t c) {
   return lo;
 }
 
-// Partial result of one element: squares and sums in 64 bits, so that neither the smallest
-// nor the largest fp32 gradient leaves the range; the magnitude's bits for the inf norm,
-// whose order as integers puts infinity above all numbers and NaN above infinity.
-__device__ __forceinline__ void take(double& sum, uint32_t& top, float g, bool inf) {
-  if (inf) top = max(top, __float_as_uint(g) & 0x7fffffffu);
-  else sum = fma(double(g), double(g), sum);
-}
-
+// 16 bytes of S elements, read and written with one access wherever they lie: a tensor may
+// start at any element (gfx950 takes unaligned 16-byte accesses; the address space keeps them
+// global, since FLAT ones would also hold up the LDS waits).
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
+typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
 template <typename S>
-__device__ __forceinline__ void norm_chunk(const S* p, int64_t n, bool inf, double& sum, uint32_t& top) {
-  for (int64_t i = threadIdx.x; i < n; i += 256) take(sum, top, ld_f(p + i), inf);
+struct Vec {
+  static constexpr int N = 16 / sizeof(S);
+  u32x4 v;
+  __device__ __forceinline__ void load(const S* p) {
+    if constexpr (sizeof(S) == 2) v = *(__attribute__((address_space(1))) const u32x4_at2*)(p);
+    else v = *(__attribute__((address_space(1))) const u32x4_at4*)(p);
+  }
+  __device__ __forceinline__ void store(S* p) const {
+    if constexpr (sizeof(S) == 2) *(__attribute__((address_space(1))) u32x4_at2*)(p) = v;
+    else *(__attribute__((address_space(1))) u32x4_at4*)(p) = v;
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(S) == 4) return __uint_as_float(v[e]);
+    else return __uint_as_float(e & 1 ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
+  }
+  // All N elements, rounded to S.
+  __device__ __forceinline__ void set(const float (&f)[N]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (sizeof(S) == 4) {
+        v[q] = __float_as_uint(f[q]);
+      } else {
+        v[q] = uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * q]))) |
+               uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(f[2 * q + 1]))) << 16;
+      }
+    }
+  }
+};
+
+// Partial result: squares and sums in 64 bits, so that neither the smallest nor the largest
+// fp32 gradient leaves the range (two sums, so that one addition need not wait for the last);
+// for the inf norm the magnitudes' bits, whose order as integers puts infinity above all
+// numbers and NaN above infinity.
+struct Part {
+  double sum[2] = {0.0, 0.0};
+  uint32_t top = 0;
+  template <bool INF>
+  __device__ __forceinline__ void take(float g, int e) {
+    if constexpr (INF) top = max(top, __float_as_uint(g) & 0x7fffffffu);
+    else sum[e & 1] = fma(double(g), double(g), sum[e & 1]);
+  }
+};
+
+// One chunk: kGradChunk bytes as four 16-byte loads per thread, all in flight before the first
+// is used; the last chunk of a tensor vector by vector, then element by element.
+template <typename S, bool INF>
+__device__ __forceinline__ void norm_chunk(const S* p, int64_t n, Part& part) {
+  constexpr int N = Vec<S>::N, U = kGradChunk / (256 * 16);
+  const int tid = threadIdx.x;
+  if (n == kGradChunk / int64_t(sizeof(S))) {
+    Vec<S> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(p + (u * 256 + tid) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < N; ++e) part.template take<INF>(x[u].get(e), e);
+    return;
+  }
+  const int vecs = int(n) / N;
+  for (int i = tid; i < vecs; i += 256) {
+    Vec<S> x;
+    x.load(p + i * N);
+#pragma unroll
+    for (int e = 0; e < N; ++e) part.template take<INF>(x.get(e), e);
+  }
+  const int i = vecs * N + tid;
+  if (i < int(n)) part.template take<INF>(ld_f(p + i), 0);
 }
 
-__global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
-  double sum = 0.0;
-  uint32_t top = 0;
+template <bool INF>
+__device__ __forceinline__ Part norm_chunks(const GradArgs& a) {
+  Part part;
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const GradRec r = a.recs[find(a.recs, a.count, c)];
     const int64_t per = r.dtype == kBF16 ? kGradChunk / 2 : kGradChunk / 4;
     const int64_t at = int64_t(c - r.first) * per;
     const int64_t n = min(per, r.n - at);
-    if (r.dtype == kBF16) norm_chunk(reinterpret_cast<const uint16_t*>(r.ptr) + at, n, a.inf, sum, top);
-    else norm_chunk(reinterpret_cast<const float*>(r.ptr) + at, n, a.inf, sum, top);
+    if (r.dtype == kBF16) norm_chunk<uint16_t, INF>(reinterpret_cast<const uint16_t*>(r.ptr) + at, n, part);
+    else norm_chunk<float, INF>(reinterpret_cast<const float*>(r.ptr) + at, n, part);
   }
+  return part;
+}
+
+__global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
+  const Part part = a.inf ? norm_chunks<true>(a) : norm_chunks<false>(a);
   __shared__ double red[256];
-  red[threadIdx.x] = a.inf ? double(top) : sum;
+  red[threadIdx.x] = a.inf ? double(part.top) : part.sum[0] + part.sum[1];
   __syncthreads();
   for (int s = 128; s > 0; s >>= 1) {
     if (int(threadIdx.x) < s) {
@@ -87,8 +156,37 @@ __global__ __launch_bounds__(256) void k_grad_norm_end(GradArgs a) {
 }
 
 template <typename S>
+__device__ __forceinline__ void scale_vec(Vec<S>& x, float coef) {
+  float f[Vec<S>::N];
+#pragma unroll
+  for (int e = 0; e < Vec<S>::N; ++e) f[e] = coef * x.get(e);
+  x.set(f);
+}
+
+template <typename S>
 __device__ __forceinline__ void clip_chunk(S* p, int64_t n, float coef) {
-  for (int64_t i = threadIdx.x; i < n; i += 256) st_f(p + i, coef * ld_f(p + i));
+  constexpr int N = Vec<S>::N, U = kGradChunk / (256 * 16);
+  const int tid = threadIdx.x;
+  if (n == kGradChunk / int64_t(sizeof(S))) {
+    Vec<S> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(p + (u * 256 + tid) * N);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      scale_vec(x[u], coef);
+      x[u].store(p + (u * 256 + tid) * N);
+    }
+    return;
+  }
+  const int vecs = int(n) / N;
+  for (int i = tid; i < vecs; i += 256) {
+    Vec<S> x;
+    x.load(p + i * N);
+    scale_vec(x, coef);
+    x.store(p + i * N);
+  }
+  const int i = vecs * N + tid;
+  if (i < int(n)) st_f(p + i, coef * ld_f(p + i));
 }
 
 __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
