@@ -3,9 +3,14 @@
 //
 // A list is a table of tensors cut into chunks (list_plan.h); a workgroup takes chunks
 // blockIdx.x, blockIdx.x + gridDim.x, ... and finds each one's tensor by a search over the
-// tensors' first chunks.  All three kernels are HBM-bound: the norm reads every gradient once,
-// clipping reads and writes it once more, AdamW reads and writes its state once.
+// tensors' first chunks.  All three kernels are HBM-bound: the norm reads every gradient once
+// (one 4096-hidden layer in bf16, 405 MB: 69.6 us, 5.8 TB/s; 512 small fp32 matrices, 1.4 GB:
+// 221 us, 6.4 TB/s), clipping reads and writes it once more (144 us, 5.6 TB/s; 488 us, 5.8
+// TB/s), AdamW reads and writes its state once.  The squares' 64-bit sums hide under the
+// loads: the inf norm, an integer maximum, takes 69.0 us on the same layer.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "list_math.h"
 #include "muon_internal.h"
@@ -21,15 +26,22 @@ __device__ __forceinline__ void st_f(uint16_t* p, float f) {
 }
 __device__ __forceinline__ void st_f(float* p, float f) { *p = f; }
 
-// The last entry whose first chunk is <= c (entries have at least one chunk each).
+// The last entry whose first chunk is <= c (entries have at least one chunk each, the first
+// entry's is 0).  The 64 lanes of a wave probe evenly spaced entries at once: a list of up to
+// 64 tensors takes one round of loads, 4096 two.
 template <typename Rec>
 __device__ __forceinline__ int find(const Rec* recs, int count, uint32_t c) {
-  int lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (recs[mid].first <= c) lo = mid; else hi = mid - 1;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = count;
+  while (len > 1) {
+    const int step = (len + 63) >> 6;
+    const int at = lane * step;
+    const bool below = at < len && recs[lo + at].first <= c;
+    const int k = __popcll(__ballot(below)) - 1;
+    lo += k * step;
+    len = min(step, len - k * step);
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // 16 bytes of S elements, read and written with one access wherever they lie: a tensor may
@@ -82,77 +94,132 @@ struct Part {
   }
 };
 
-// One chunk: kGradChunk bytes as four 16-byte loads per thread, all in flight before the first
-// is used; the last chunk of a tensor vector by vector, then element by element.
-template <typename S, bool INF>
-__device__ __forceinline__ void norm_chunk(const S* p, int64_t n, Part& part) {
-  constexpr int N = Vec<S>::N, U = kGradChunk / (256 * 16);
+// A piece of a chunk: the elements [lo, hi) of the BYTES bytes behind p.  Chunks start on line
+// boundaries, the first one at or before its tensor, so lanes read and write whole lines
+// wherever the tensor starts (with chunks counted from the tensor's own start, an odd one cost
+// 13 % on a bf16 norm).
+template <typename S, int BYTES>
+struct Piece {
+  S* p;
+  int lo, hi;
+  static constexpr int kAll = BYTES / int(sizeof(S));
+};
+// Piece h of chunk c of the tensor; empty (hi <= lo) behind the tensor's end.
+template <typename S, int BYTES>
+__device__ __forceinline__ Piece<S, BYTES> piece_of(const GradRec& r, uint32_t c, int h = 0) {
+  const int shift = int(r.ptr % kLine / sizeof(S));
+  const int64_t at = int64_t(c - r.first) * (kGradChunk / int64_t(sizeof(S))) + h * Piece<S, BYTES>::kAll - shift;
+  Piece<S, BYTES> x;
+  x.p = reinterpret_cast<S*>(r.ptr) + at;
+  x.lo = at < 0 ? int(-at) : 0;
+  x.hi = int(min(int64_t(Piece<S, BYTES>::kAll), r.n - at));
+  return x;
+}
+
+// f(vector) for each of this thread's vectors of a piece; STORE: write them back.  A whole
+// piece has all its loads in flight before the first vector is used; else vectors that reach
+// outside go element by element (with zeros for what is outside, which change neither a sum
+// nor a maximum).
+template <bool STORE, typename S, int BYTES, typename F>
+__device__ __forceinline__ void each_vec(const Piece<S, BYTES>& x, F&& f) {
+  constexpr int N = Vec<S>::N, U = BYTES / (256 * 16);
   const int tid = threadIdx.x;
-  if (n == kGradChunk / int64_t(sizeof(S))) {
-    Vec<S> x[U];
+  if (x.lo == 0 && x.hi == x.kAll) {
+    Vec<S> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(p + (u * 256 + tid) * N);
+    for (int u = 0; u < U; ++u) v[u].load(x.p + (u * 256 + tid) * N);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < N; ++e) part.template take<INF>(x[u].get(e), e);
+    for (int u = 0; u < U; ++u) {
+      f(v[u]);
+      if (STORE) v[u].store(x.p + (u * 256 + tid) * N);
+    }
     return;
   }
-  const int vecs = int(n) / N;
-  for (int i = tid; i < vecs; i += 256) {
-    Vec<S> x;
-    x.load(p + i * N);
+  for (int i = tid * N; i < x.hi; i += 256 * N) {
+    Vec<S> v;
+    if (i >= x.lo && i + N <= x.hi) {
+      v.load(x.p + i);
+      f(v);
+      if (STORE) v.store(x.p + i);
+      continue;
+    }
+    float e[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) part.template take<INF>(x.get(e), e);
+    for (int k = 0; k < N; ++k) e[k] = i + k >= x.lo && i + k < x.hi ? ld_f(x.p + i + k) : 0.0f;
+    v.set(e);
+    f(v);
+    if (STORE) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (i + k >= x.lo && i + k < x.hi) st_f(x.p + i + k, v.get(k));
+    }
   }
-  const int i = vecs * N + tid;
-  if (i < int(n)) part.template take<INF>(ld_f(p + i), 0);
 }
 
 template <bool INF>
 __device__ __forceinline__ Part norm_chunks(const GradArgs& a) {
   Part part;
+  auto take = [&](const auto& v) {
+#pragma unroll
+    for (int e = 0; e < std::decay_t<decltype(v)>::N; ++e) part.template take<INF>(v.get(e), e);
+  };
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const GradRec r = a.recs[find(a.recs, a.count, c)];
-    const int64_t per = r.dtype == kBF16 ? kGradChunk / 2 : kGradChunk / 4;
-    const int64_t at = int64_t(c - r.first) * per;
-    const int64_t n = min(per, r.n - at);
-    if (r.dtype == kBF16) norm_chunk<uint16_t, INF>(reinterpret_cast<const uint16_t*>(r.ptr) + at, n, part);
-    else norm_chunk<float, INF>(reinterpret_cast<const float*>(r.ptr) + at, n, part);
+    if (r.dtype == kBF16) each_vec<false>(piece_of<uint16_t, kGradChunk>(r, c), take);
+    else each_vec<false>(piece_of<float, kGradChunk>(r, c), take);
   }
   return part;
 }
 
-__global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
-  const Part part = a.inf ? norm_chunks<true>(a) : norm_chunks<false>(a);
-  __shared__ double red[256];
-  red[threadIdx.x] = a.inf ? double(part.top) : part.sum[0] + part.sum[1];
+// Sum, or maximum, over a workgroup in a fixed order; the result is thread 0's.
+__device__ __forceinline__ double combine(double x, double y, bool inf) { return inf ? (x > y ? x : y) : x + y; }
+__device__ __forceinline__ double reduce(double x, bool inf, double* red) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = combine(x, __shfl_xor(x, off, 64), inf);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
   __syncthreads();
-  for (int s = 128; s > 0; s >>= 1) {
-    if (int(threadIdx.x) < s) {
-      const double x = red[threadIdx.x], y = red[threadIdx.x + s];
-      red[threadIdx.x] = a.inf ? (x > y ? x : y) : x + y;
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) a.parts[blockIdx.x] = red[0];
+  return combine(combine(red[0], red[1], inf), combine(red[2], red[3], inf), inf);
 }
 
-// The partial results' sum (or maximum) in a fixed order, and the norm.
-__global__ __launch_bounds__(256) void k_grad_norm_end(GradArgs a) {
-  __shared__ double red[256];
-  double x = 0.0;
-  for (int i = threadIdx.x; i < a.nparts; i += 256) x = a.inf ? (a.parts[i] > x ? a.parts[i] : x) : x + a.parts[i];
-  red[threadIdx.x] = x;
-  __syncthreads();
-  for (int s = 128; s > 0; s >>= 1) {
-    if (int(threadIdx.x) < s) {
-      const double u = red[threadIdx.x], w = red[threadIdx.x + s];
-      red[threadIdx.x] = a.inf ? (u > w ? u : w) : u + w;
+// The workgroup that finishes last adds up all partial results, always in the same order, so
+// one launch does the whole norm.  Partial results pass between XCDs, whose L2s are not
+// coherent with each other: they are stored and loaded at device scope, and a store is
+// complete (s_waitcnt) before its workgroup counts itself.  No device-wide release: it writes
+// back a whole L2, and one per workgroup took 36 us over 1024 workgroups.  Counts of one
+// address are made one after another (10 ns each), so a workgroup counts itself among those
+// with its index modulo kTickets, and the last of each of these among the last ones.  All
+// counts are back at 0 at the end.
+__device__ __forceinline__ uint32_t count_self(uint32_t* ticket) {
+  return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
+  __shared__ double red[4], red_all[4];
+  __shared__ bool last;
+  const bool inf = a.inf;
+  const Part part = inf ? norm_chunks<true>(a) : norm_chunks<false>(a);
+  double x = reduce(inf ? double(part.top) : part.sum[0] + part.sum[1], inf, red);
+  const unsigned grid = gridDim.x;
+  if (grid > 1) {
+    if (threadIdx.x == 0) {
+      __hip_atomic_store(a.parts + blockIdx.x, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __builtin_amdgcn_s_waitcnt(0);
+      const unsigned mine = blockIdx.x % kTickets;
+      uint32_t* ticket = a.tickets + (1 + mine) * (kLine / 4);
+      last = count_self(ticket) == (grid - mine - 1) / kTickets;
+      if (last) {
+        __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        last = count_self(a.tickets) == min(grid, unsigned(kTickets)) - 1;
+        if (last) __hip_atomic_store(a.tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
     __syncthreads();
+    if (!last) return;
+    x = 0.0;
+    for (unsigned i = threadIdx.x; i < grid; i += 256)
+      x = combine(x, __hip_atomic_load(a.parts + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), inf);
+    x = reduce(x, inf, red_all);
   }
-  if (threadIdx.x == 0) *a.norm = a.inf ? __uint_as_float(uint32_t(red[0])) : float(sqrt(red[0]));
+  if (threadIdx.x == 0) *a.norm = inf ? __uint_as_float(uint32_t(x)) : float(sqrt(x));
 }
 
 template <typename S>
@@ -163,42 +230,19 @@ __device__ __forceinline__ void scale_vec(Vec<S>& x, float coef) {
   x.set(f);
 }
 
-template <typename S>
-__device__ __forceinline__ void clip_chunk(S* p, int64_t n, float coef) {
-  constexpr int N = Vec<S>::N, U = kGradChunk / (256 * 16);
-  const int tid = threadIdx.x;
-  if (n == kGradChunk / int64_t(sizeof(S))) {
-    Vec<S> x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(p + (u * 256 + tid) * N);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      scale_vec(x[u], coef);
-      x[u].store(p + (u * 256 + tid) * N);
-    }
-    return;
-  }
-  const int vecs = int(n) / N;
-  for (int i = tid; i < vecs; i += 256) {
-    Vec<S> x;
-    x.load(p + i * N);
-    scale_vec(x, coef);
-    x.store(p + i * N);
-  }
-  const int i = vecs * N + tid;
-  if (i < int(n)) st_f(p + i, coef * ld_f(p + i));
-}
-
 __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
   const float coef = clip_coef(a.clip);
   if (coef == 1.0f) return;
-  for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+  auto scale = [=](auto& v) { scale_vec(v, coef); };
+  // By half chunks (512 small fp32 matrices, 1.4 GB: 488 us by 16 KiB, 534 by 32 KiB, 576 by
+  // 8 KiB), a workgroup each up to 65536 of them (2048 looping ones: 538), and backwards, since
+  // what the norm read last may still be in the memory-side cache (1 % of a layer's clipping).
+  for (uint32_t b = blockIdx.x; b < 2 * a.chunks; b += gridDim.x) {
+    const uint32_t h = 2 * a.chunks - 1 - b;
+    const uint32_t c = h >> 1;
     const GradRec r = a.recs[find(a.recs, a.count, c)];
-    const int64_t per = r.dtype == kBF16 ? kGradChunk / 2 : kGradChunk / 4;
-    const int64_t at = int64_t(c - r.first) * per;
-    const int64_t n = min(per, r.n - at);
-    if (r.dtype == kBF16) clip_chunk(reinterpret_cast<uint16_t*>(r.ptr) + at, n, coef);
-    else clip_chunk(reinterpret_cast<float*>(r.ptr) + at, n, coef);
+    if (r.dtype == kBF16) each_vec<true>(piece_of<uint16_t, kGradChunk / 2>(r, c, h & 1), scale);
+    else each_vec<true>(piece_of<float, kGradChunk / 2>(r, c, h & 1), scale);
   }
 }
 
@@ -246,22 +290,15 @@ unsigned grid_of(uint32_t chunks, uint32_t most) { return chunks < most ? chunks
 
 }  // namespace
 
-int muon_launch_grad_norm(const GradArgs& args, void* stream) {
-  GradArgs a = args;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  a.nparts = int32_t(grid_of(a.chunks, kNormParts));
-  if (a.nparts > 0) {
-    hipLaunchKernelGGL(k_grad_norm, dim3(unsigned(a.nparts)), dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(k_grad_norm_end, dim3(1), dim3(256), 0, s, a);
+int muon_launch_grad_norm(const GradArgs& a, void* stream) {
+  const unsigned grid = a.chunks ? grid_of(a.chunks, kNormParts) : 1;  // no gradients: the norm is 0
+  hipLaunchKernelGGL(k_grad_norm, dim3(grid), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return hipGetLastError();
 }
 
 int muon_launch_grad_clip(const GradArgs& a, void* stream) {
   if (a.chunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_grad_clip, dim3(grid_of(a.chunks, 1u << 16)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  hipLaunchKernelGGL(k_grad_clip, dim3(grid_of(2 * a.chunks, 1u << 16)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return hipGetLastError();
 }
 

@@ -89,7 +89,8 @@ int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::st
     if (uintptr_t(x.n) * uintptr_t(es) > UINTPTR_MAX - p) return refuse(err, MUON_EINVAL, i, "buffer passes the end of memory");
     spans.push_back({p, p + uintptr_t(x.n) * uintptr_t(es), i, true});
     recs.push_back({uint64_t(p), x.n, uint32_t(chunks), uint32_t(x.dtype)});
-    chunks += uint64_t(ceil_div(x.n * es, kGradChunk));
+    // Chunks start on line boundaries, the first one at or before the tensor.
+    chunks += uint64_t(ceil_div(x.n * es + int64_t(p % uintptr_t(kLine)), kGradChunk));
     t->elems += x.n;
     t->read_bytes += double(x.n) * es;
   }

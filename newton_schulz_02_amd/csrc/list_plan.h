@@ -4,8 +4,8 @@
 // A list's chunks are numbered through: tensor i owns the chunks [first_i, first_{i+1}), the
 // last of each tensor being partial.  Empty tensors have no entry.  Tables are written to the
 // caller's workspace once (the *_init calls) and only read afterwards:
-//   head (256 bytes: status word, the norm's ticket), entries, and for a gradient list the
-//   norm's partial results.
+//   head (status word, the norm's counts), entries, and for a gradient list the norm's
+//   partial results.
 #pragma once
 
 #include <cstdint>

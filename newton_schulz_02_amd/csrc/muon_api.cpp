@@ -969,6 +969,7 @@ GradArgs grad_args(const ListHandle& h) {
   a.recs = reinterpret_cast<const GradRec*>(ws + kListHead);
   a.count = h.entries;
   a.chunks = h.chunks;
+  a.tickets = reinterpret_cast<uint32_t*>(ws + kListTickets);
   a.parts = reinterpret_cast<double*>(ws + round_up(kListHead + int64_t(h.entries) * int64_t(sizeof(GradRec)), 256));
   return a;
 }
