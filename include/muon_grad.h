@@ -29,7 +29,7 @@
  * is rounded once.  Without a master that rounding loses updates below half a bf16 step.
  *
  * Lists: a list is laid out once (muon_grad_list_init, adamw_list_init: the tensors'
- * addresses and sizes go to the caller's workspace) and then used by any number of calls, as
+ * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used by any number of calls, as
  * long as the tensors stay where they are; their values may change.  The layout is enqueued
  * on the stream given (through kernel arguments: no host buffer, no copy, so it may be
  * captured); uses on another stream must be ordered after it by the caller.  Two calls in

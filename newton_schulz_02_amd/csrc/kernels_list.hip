@@ -2,12 +2,15 @@
 // AdamW (muon_grad.h).
 //
 // A list is a table of tensors cut into chunks (list_plan.h); a workgroup takes chunks
-// blockIdx.x, blockIdx.x + gridDim.x, ... and finds each one's tensor by a search over the
-// tensors' first chunks.  All three kernels are HBM-bound: the norm reads every gradient once
-// (one 4096-hidden layer in bf16, 405 MB: 69.6 us, 5.8 TB/s; 512 small fp32 matrices, 1.4 GB:
-// 221 us, 6.4 TB/s), clipping reads and writes it once more (144 us, 5.6 TB/s; 488 us, 5.8
-// TB/s), AdamW reads and writes its state once.  The squares' 64-bit sums hide under the
-// loads: the inf norm, an integer maximum, takes 69.0 us on the same layer.
+// blockIdx.x, blockIdx.x + gridDim.x, ... and finds each one's tensor in the list's map.  All
+// three kernels are HBM-bound:
+//   norm   reads every gradient once: one 4096-hidden layer in bf16 (405 MB) in 61.5 us, 6.6
+//          TB/s; 512 small fp32 matrices (1.4 GB) in 200 us, 7.0 TB/s.  The squares' 64-bit
+//          sums hide under the loads: the inf norm, an integer maximum, is 1 % faster.
+//   clip   reads and writes them: 126 us, 6.4 TB/s; 450 us, 6.3 TB/s.
+//   AdamW  reads and writes its state once: two 32000 x 4096 embeddings with masters and bf16
+//          gradients (7.3 GB) in 1.23 ms, 6.0 TB/s.
+// (A copy by the runtime's own kernel moves 4.9 TB/s on the same card.)
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -26,27 +29,28 @@ __device__ __forceinline__ void st_f(uint16_t* p, float f) {
 }
 __device__ __forceinline__ void st_f(float* p, float f) { *p = f; }
 
-// The last entry whose first chunk is <= c (entries have at least one chunk each, the first
-// entry's is 0).  The 64 lanes of a wave probe evenly spaced entries at once: a list of up to
-// 64 tensors takes one round of loads, 4096 two.
+// map[c] <- the tensor of chunk c: the last entry whose first chunk is <= c (entries have at
+// least one chunk each, the first entry's is 0).  Run once per list, so that the kernels below
+// find a chunk's tensor by one load: a search there, three loads one behind the other, was a
+// third of a workgroup's time in AdamW over 1000 tensors.
 template <typename Rec>
-__device__ __forceinline__ int find(const Rec* recs, int count, uint32_t c) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, len = count;
-  while (len > 1) {
-    const int step = (len + 63) >> 6;
-    const int at = lane * step;
-    const bool below = at < len && recs[lo + at].first <= c;
-    const int k = __popcll(__ballot(below)) - 1;
-    lo += k * step;
-    len = min(step, len - k * step);
+__global__ __launch_bounds__(256) void k_list_map(const Rec* recs, int count, uint32_t chunks, uint32_t* map) {
+  const uint32_t step = gridDim.x * 256u;
+  for (uint64_t c = blockIdx.x * 256u + threadIdx.x; c < chunks; c += step) {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (recs[mid].first <= c) lo = mid; else hi = mid - 1;
+    }
+    map[c] = uint32_t(lo);
   }
-  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // 16 bytes of S elements, read and written with one access wherever they lie: a tensor may
 // start at any element (gfx950 takes unaligned 16-byte accesses; the address space keeps them
-// global, since FLAT ones would also hold up the LDS waits).
+// global, since FLAT ones would also hold up the LDS waits).  Non-temporal, as every list
+// access below: nothing is used twice by one kernel.  That is worth a tenth: the norm of a bf16
+// layer takes 63.6 us with it and 70.4 us without, its clipping 126 and 145 us.
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
 typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
@@ -55,12 +59,12 @@ struct Vec {
   static constexpr int N = 16 / sizeof(S);
   u32x4 v;
   __device__ __forceinline__ void load(const S* p) {
-    if constexpr (sizeof(S) == 2) v = *(__attribute__((address_space(1))) const u32x4_at2*)(p);
-    else v = *(__attribute__((address_space(1))) const u32x4_at4*)(p);
+    if constexpr (sizeof(S) == 2) v = __builtin_nontemporal_load((__attribute__((address_space(1))) const u32x4_at2*)(p));
+    else v = __builtin_nontemporal_load((__attribute__((address_space(1))) const u32x4_at4*)(p));
   }
   __device__ __forceinline__ void store(S* p) const {
-    if constexpr (sizeof(S) == 2) *(__attribute__((address_space(1))) u32x4_at2*)(p) = v;
-    else *(__attribute__((address_space(1))) u32x4_at4*)(p) = v;
+    if constexpr (sizeof(S) == 2) __builtin_nontemporal_store(v, (__attribute__((address_space(1))) u32x4_at2*)(p));
+    else __builtin_nontemporal_store(v, (__attribute__((address_space(1))) u32x4_at4*)(p));
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (sizeof(S) == 4) return __uint_as_float(v[e]);
@@ -164,7 +168,7 @@ __device__ __forceinline__ Part norm_chunks(const GradArgs& a) {
     for (int e = 0; e < std::decay_t<decltype(v)>::N; ++e) part.template take<INF>(v.get(e), e);
   };
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const GradRec r = a.recs[find(a.recs, a.count, c)];
+    const GradRec r = a.recs[a.map[c]];
     if (r.dtype == kBF16) each_vec<false>(piece_of<uint16_t, kGradChunk>(r, c), take);
     else each_vec<false>(piece_of<float, kGradChunk>(r, c), take);
   }
@@ -234,61 +238,169 @@ __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
   const float coef = clip_coef(a.clip);
   if (coef == 1.0f) return;
   auto scale = [=](auto& v) { scale_vec(v, coef); };
-  // By half chunks (512 small fp32 matrices, 1.4 GB: 488 us by 16 KiB, 534 by 32 KiB, 576 by
-  // 8 KiB), a workgroup each up to 65536 of them (2048 looping ones: 538), and backwards, since
-  // what the norm read last may still be in the memory-side cache (1 % of a layer's clipping).
+  // By half chunks (512 small fp32 matrices, 1.4 GB: 450 us by 16 KiB, 475 by 32 KiB and by
+  // 8 KiB), a workgroup each, and backwards, since what the norm read last may still be in the
+  // memory-side cache (1 % of a layer's clipping).
   for (uint32_t b = blockIdx.x; b < 2 * a.chunks; b += gridDim.x) {
     const uint32_t h = 2 * a.chunks - 1 - b;
     const uint32_t c = h >> 1;
-    const GradRec r = a.recs[find(a.recs, a.count, c)];
+    const GradRec r = a.recs[a.map[c]];
     if (r.dtype == kBF16) each_vec<true>(piece_of<uint16_t, kGradChunk / 2>(r, c, h & 1), scale);
     else each_vec<true>(piece_of<float, kGradChunk / 2>(r, c, h & 1), scale);
   }
 }
 
-// n elements from element `at` of one tensor; a master takes the place of the param as what
-// is updated.
+// Four neighbouring elements, as one access at any alignment (16 bytes of fp32, 8 of bf16), or
+// those of them in [lo, hi) one by one.
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 __attribute__((aligned(2))) u32x2_at2;
+typedef uint16_t bf16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void load4(const float* p, float (&f)[4]) {
+  const u32x4 v = __builtin_nontemporal_load((__attribute__((address_space(1))) const u32x4_at4*)(p));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(v[k]);
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float (&f)[4]) {
+  const u32x2 v = __builtin_nontemporal_load((__attribute__((address_space(1))) const u32x2_at2*)(p));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(k & 1 ? v[k >> 1] & 0xffff0000u : v[k >> 1] << 16);
+}
+__device__ __forceinline__ void store4(float* p, const float (&f)[4]) {
+  u32x4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __float_as_uint(f[k]);
+  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) u32x4_at4*)(p));
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
+  bf16x4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[k]));
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x2, v), (__attribute__((address_space(1))) u32x2_at2*)(p));
+}
+template <typename S>
+__device__ __forceinline__ void load_some(const S* p, float (&f)[4], int i, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = i + k >= lo && i + k < hi ? ld_f(p + i + k) : 0.0f;
+}
+template <typename S>
+__device__ __forceinline__ void store_some(S* p, const float (&f)[4], int i, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (i + k >= lo && i + k < hi) st_f(p + i + k, f[k]);
+}
+
+// The elements of chunk c of one tensor; a master takes the place of the param as what is
+// updated.  Chunks start where m lies on a line boundary, so buffers that lie alike (those of
+// one flat bucket per type) are all read and written by whole lines.
+// All loads of a whole chunk are in flight before the first update: 16 bytes of fp32 per lane
+// and load, two of each buffer.  Non-temporal loads and stores together are worth a tenth
+// (embeddings with masters 1.36 -> 1.23 ms), either alone nothing.  Dividing by reciprocals
+// instead changes nothing: the arithmetic hides under the loads.
 template <typename P, typename G, bool MASTER>
-__device__ __forceinline__ void adamw_chunk(const AdamRec& r, int64_t at, int64_t n, float coef,
-                                            const AdamListArgs& a) {
+__device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float coef, const AdamListArgs& a) {
+  typedef std::conditional_t<MASTER, float, P> X;
+  const int64_t at = int64_t(c - r.first) * kAdamChunk - int64_t(r.m % kLine / 4);
   P* p = reinterpret_cast<P*>(r.param) + at;
+  X* x = reinterpret_cast<X*>(MASTER ? r.master : r.param) + at;
   const G* g = reinterpret_cast<const G*>(r.grad) + at;
   float* m = reinterpret_cast<float*>(r.m) + at;
   float* v = reinterpret_cast<float*>(r.v) + at;
-  float* w = reinterpret_cast<float*>(r.master) + at;
   const float wd = a.wd * r.decay;
-  for (int64_t i = threadIdx.x; i < n; i += 256) {
-    float x = MASTER ? w[i] : ld_f(p + i), mi = m[i], vi = v[i];
-    adamw_one(x, coef * ld_f(g + i), mi, vi, a, wd);
-    m[i] = mi;
-    v[i] = vi;
-    if (MASTER) w[i] = x;
-    st_f(p + i, x);
+  const int tid = threadIdx.x;
+  constexpr int U = int(kAdamChunk) / 1024;
+  if (at >= 0 && r.n - at >= kAdamChunk) {
+    float xs[U][4], gs[U][4], ms[U][4], vs[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = (u * 256 + tid) * 4;
+      load4(x + i, xs[u]);
+      load4(g + i, gs[u]);
+      load4(m + i, ms[u]);
+      load4(v + i, vs[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = (u * 256 + tid) * 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, wd);
+      store4(m + i, ms[u]);
+      store4(v + i, vs[u]);
+      store4(x + i, xs[u]);
+      if (MASTER) store4(p + i, xs[u]);
+    }
+    return;
+  }
+  const int lo = at < 0 ? int(-at) : 0;
+  const int hi = int(min(kAdamChunk, r.n - at));
+  for (int i = tid * 4; i < hi; i += 1024) {
+    if (i + 4 <= lo) continue;
+    const bool all = i >= lo && i + 4 <= hi;
+    float xs[4], gs[4], ms[4], vs[4];
+    if (all) {
+      load4(x + i, xs);
+      load4(g + i, gs);
+      load4(m + i, ms);
+      load4(v + i, vs);
+    } else {
+      load_some(x, xs, i, lo, hi);
+      load_some(g, gs, i, lo, hi);
+      load_some(m, ms, i, lo, hi);
+      load_some(v, vs, i, lo, hi);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) adamw_one(xs[k], coef * gs[k], ms[k], vs[k], a, wd);
+    if (all) {
+      store4(m + i, ms);
+      store4(v + i, vs);
+      store4(x + i, xs);
+      if (MASTER) store4(p + i, xs);
+    } else {
+      store_some(m, ms, i, lo, hi);
+      store_some(v, vs, i, lo, hi);
+      store_some(x, xs, i, lo, hi);
+      if (MASTER) store_some(p, xs, i, lo, hi);
+    }
   }
 }
 
 __global__ __launch_bounds__(256) void k_adamw_list(AdamListArgs a) {
   const float coef = clip_coef(a.clip);
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const AdamRec& r = a.recs[find(a.recs, a.count, c)];
-    const int64_t at = int64_t(c - r.first) * kAdamChunk;
-    const int64_t n = min(kAdamChunk, r.n - at);
+    const AdamRec& r = a.recs[a.map[c]];
     if (!r.param_bf16) {
-      if (r.grad_bf16) adamw_chunk<float, uint16_t, false>(r, at, n, coef, a);
-      else adamw_chunk<float, float, false>(r, at, n, coef, a);
+      if (r.grad_bf16) adamw_chunk<float, uint16_t, false>(r, c, coef, a);
+      else adamw_chunk<float, float, false>(r, c, coef, a);
     } else if (r.master) {
-      if (r.grad_bf16) adamw_chunk<uint16_t, uint16_t, true>(r, at, n, coef, a);
-      else adamw_chunk<uint16_t, float, true>(r, at, n, coef, a);
+      if (r.grad_bf16) adamw_chunk<uint16_t, uint16_t, true>(r, c, coef, a);
+      else adamw_chunk<uint16_t, float, true>(r, c, coef, a);
     } else {
-      if (r.grad_bf16) adamw_chunk<uint16_t, uint16_t, false>(r, at, n, coef, a);
-      else adamw_chunk<uint16_t, float, false>(r, at, n, coef, a);
+      if (r.grad_bf16) adamw_chunk<uint16_t, uint16_t, false>(r, c, coef, a);
+      else adamw_chunk<uint16_t, float, false>(r, c, coef, a);
     }
   }
 }
 
+// A workgroup for each chunk: looping over chunks with 2048 or 4096 workgroups cost AdamW and
+// clipping a tenth, since a looping wave's loads wait behind its stores.
+constexpr uint32_t kMostGroups = 1u << 20;
 unsigned grid_of(uint32_t chunks, uint32_t most) { return chunks < most ? chunks : most; }
 
+template <typename Rec>
+int launch_map(const Rec* recs, int count, uint32_t chunks, uint32_t* map, void* stream) {
+  if (chunks == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_list_map<Rec>, dim3(grid_of(uint32_t(ceil_div(chunks, 256)), 4096)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), recs, count, chunks, map);
+  return hipGetLastError();
+}
+
 }  // namespace
+
+int muon_launch_grad_map(const GradRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream) {
+  return launch_map(recs, count, chunks, map, stream);
+}
+int muon_launch_adamw_map(const AdamRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream) {
+  return launch_map(recs, count, chunks, map, stream);
+}
 
 int muon_launch_grad_norm(const GradArgs& a, void* stream) {
   const unsigned grid = a.chunks ? grid_of(a.chunks, kNormParts) : 1;  // no gradients: the norm is 0
@@ -298,12 +410,12 @@ int muon_launch_grad_norm(const GradArgs& a, void* stream) {
 
 int muon_launch_grad_clip(const GradArgs& a, void* stream) {
   if (a.chunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_grad_clip, dim3(grid_of(2 * a.chunks, 1u << 16)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  hipLaunchKernelGGL(k_grad_clip, dim3(grid_of(2 * a.chunks, kMostGroups)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return hipGetLastError();
 }
 
 int muon_launch_adamw_list(const AdamListArgs& a, void* stream) {
   if (a.chunks == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_adamw_list, dim3(grid_of(a.chunks, 1u << 16)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
+  hipLaunchKernelGGL(k_adamw_list, dim3(grid_of(a.chunks, kMostGroups)), dim3(256), 0, static_cast<hipStream_t>(stream), a);
   return hipGetLastError();
 }

@@ -53,7 +53,9 @@ void lay_out(const std::vector<Rec>& recs, ListTable* t) {
   t->entries = int32_t(recs.size());
   t->words.assign((kListHead + recs.size() * sizeof(Rec)) / 4, 0);
   if (!recs.empty()) std::memcpy(t->words.data() + kListHead / 4, recs.data(), recs.size() * sizeof(Rec));
-  t->ws_bytes = size_t(round_up(int64_t(t->words.size()) * 4, 256));
+  t->map_off = size_t(round_up(int64_t(t->words.size()) * 4, 256));
+  t->parts_off = t->map_off + size_t(round_up(int64_t(t->chunks) * 4, 256));
+  t->ws_bytes = t->parts_off;
 }
 
 int check_count(const void* list, int32_t count, std::string* err) {
@@ -149,7 +151,8 @@ int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, s
     r.grad_bf16 = x.grad_dtype == MUON_BF16;
     r.decay = x.decay;
     recs.push_back(r);
-    chunks += uint64_t(ceil_div(x.n, kAdamChunk));
+    // Chunks start where m lies on a line boundary, the first one at or before the tensor.
+    chunks += uint64_t(ceil_div(x.n + int64_t(r.m % uint64_t(kLine) / 4), kAdamChunk));
     t->elems += x.n;
   }
   if ((rc = check_spans(spans, err)) != MUON_OK) return rc;

@@ -4,8 +4,8 @@
 // A list's chunks are numbered through: tensor i owns the chunks [first_i, first_{i+1}), the
 // last of each tensor being partial.  Empty tensors have no entry.  Tables are written to the
 // caller's workspace once (the *_init calls) and only read afterwards:
-//   head (status word, the norm's counts), entries, and for a gradient list the norm's
-//   partial results.
+//   head (status word, the norm's counts), entries, the map (the entry of each chunk, filled
+//   by a kernel), and for a gradient list the norm's partial results.
 #pragma once
 
 #include <cstdint>
@@ -27,6 +27,7 @@ struct ListTable {
   int64_t elems = 0;
   double read_bytes = 0.0;      // gradients (all operands of an AdamW list) read once
   double write_bytes = 0.0;     // outputs written once
+  size_t map_off = 0, parts_off = 0;  // bytes from the workspace's start
   size_t ws_bytes = 0;
 };
 
@@ -39,10 +40,8 @@ struct ListHandle {
   uint64_t magic;     // kind of list
   uint64_t workspace;
   uint32_t chunks;
-  int32_t entries;
   int32_t device;
-  int32_t reserved;
-  int64_t elems;
+  uint64_t map_off, parts_off;
   double read_bytes, write_bytes;
   uint64_t check;     // over the fields above: an uninitialised or foreign handle is refused
 };

@@ -906,12 +906,18 @@ int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t worksp
   if ((rc = check_device(dev)) != MUON_OK) return rc;
   const int e = muon_put_words(workspace, t.words.data(), t.words.size() * 4, hip_stream);
   if (e != hipSuccess) return hip_fail(hipError_t(e), "list layout (kernel arguments)");
+  char* ws = static_cast<char*>(workspace);
+  uint32_t* map = reinterpret_cast<uint32_t*>(ws + t.map_off);
+  const int em = magic == kGradListMagic
+                     ? muon_launch_grad_map(reinterpret_cast<const GradRec*>(ws + kListHead), t.entries, t.chunks, map, hip_stream)
+                     : muon_launch_adamw_map(reinterpret_cast<const AdamRec*>(ws + kListHead), t.entries, t.chunks, map, hip_stream);
+  if (em != hipSuccess) return hip_fail(hipError_t(em), "list layout (map)");
   h.magic = magic;
   h.workspace = uint64_t(reinterpret_cast<uintptr_t>(workspace));
   h.chunks = t.chunks;
-  h.entries = t.entries;
   h.device = dev;
-  h.elems = t.elems;
+  h.map_off = t.map_off;
+  h.parts_off = t.parts_off;
   h.read_bytes = t.read_bytes;
   h.write_bytes = t.write_bytes;
   h.check = handle_check(h);
@@ -967,10 +973,10 @@ GradArgs grad_args(const ListHandle& h) {
   std::memset(&a, 0, sizeof a);
   char* ws = reinterpret_cast<char*>(uintptr_t(h.workspace));
   a.recs = reinterpret_cast<const GradRec*>(ws + kListHead);
-  a.count = h.entries;
+  a.map = reinterpret_cast<const uint32_t*>(ws + h.map_off);
   a.chunks = h.chunks;
   a.tickets = reinterpret_cast<uint32_t*>(ws + kListTickets);
-  a.parts = reinterpret_cast<double*>(ws + round_up(kListHead + int64_t(h.entries) * int64_t(sizeof(GradRec)), 256));
+  a.parts = reinterpret_cast<double*>(ws + h.parts_off);
   return a;
 }
 
@@ -1110,8 +1116,9 @@ int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_
     if (clip && (rc = check_clip(clip)) != MUON_OK) return rc;
     AdamListArgs a;
     std::memset(&a, 0, sizeof a);
-    a.recs = reinterpret_cast<const AdamRec*>(uintptr_t(h.workspace) + uintptr_t(kListHead));
-    a.count = h.entries;
+    const char* ws = reinterpret_cast<const char*>(uintptr_t(h.workspace));
+    a.recs = reinterpret_cast<const AdamRec*>(ws + kListHead);
+    a.map = reinterpret_cast<const uint32_t*>(ws + h.map_off);
     a.chunks = h.chunks;
     if (clip) a.clip = {clip->norm, clip->max_norm};
     a.lr = hp->lr;

@@ -181,11 +181,14 @@ constexpr int kTickets = 8;            // groups in which a norm's workgroups co
 constexpr int64_t kListTickets = 256;  // a list's workspace: status word, counts, entries
 constexpr int64_t kListHead = kListTickets + (kTickets + 1) * kLine;
 constexpr int64_t kGradChunk = 32768;  // bytes of one chunk of a gradient list
-constexpr int64_t kAdamChunk = 2048;   // elements of one chunk of an AdamW list
-// Most workgroups (and partial results) of a norm.  With 32 KiB chunks, us of a 4096-hidden
-// layer in bf16 and of 512 small fp32 matrices: 512 workgroups 68.6 and 252, 1024 69.6 and 222,
-// 2048 74.2 and 235; 16 KiB chunks with 1024 68.0 and 245, with 2048 71.2 and 222.
-constexpr int kNormParts = 1024;
+// Elements of one chunk of an AdamW list: 2048 against 1024, us: bf16 param and gradient
+// 469 / 498, fp32 305 / 300, bf16 with master 1231 / 1201; 4096 is slower for all.
+constexpr int64_t kAdamChunk = 2048;
+// Most workgroups (and partial results) of a norm: a few long ones, each 32 KiB of loads ahead.
+// us of a 4096-hidden layer in bf16 / of 512 small fp32 matrices: 512 workgroups 61.5 / 200,
+// 768 63.4 / 205, 1024 64.1 / 207, 2048 69.8 / 223; 16 KiB chunks with 1024 63.4 / 204; 64 KiB
+// with 512 65.7 / 208.
+constexpr int kNormParts = 512;
 
 struct GradRec {
   uint64_t ptr;
@@ -211,7 +214,7 @@ struct ClipArg {
 
 struct GradArgs {
   const GradRec* recs;
-  int32_t count;
+  const uint32_t* map;  // tensor of each chunk
   uint32_t chunks;
   double* parts;     // one per workgroup of the norm
   uint32_t* tickets; // counts of the norm's workgroups that are done; 0 between launches
@@ -222,7 +225,7 @@ struct GradArgs {
 
 struct AdamListArgs {
   const AdamRec* recs;
-  int32_t count;
+  const uint32_t* map;  // tensor of each chunk
   uint32_t chunks;
   ClipArg clip;
   float lr, beta1, beta2, eps, wd;
@@ -242,6 +245,8 @@ int muon_launch_gemm_deep(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_gemm_small(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_gemm_wide(const muon::GemmArgs& a, int dtype, void* stream);
 int muon_launch_adamw(const muon::AdamArgs& a, void* stream);
+int muon_launch_grad_map(const muon::GradRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream);
+int muon_launch_adamw_map(const muon::AdamRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream);
 int muon_launch_grad_norm(const muon::GradArgs& a, void* stream);
 int muon_launch_grad_clip(const muon::GradArgs& a, void* stream);
 int muon_launch_adamw_list(const muon::AdamListArgs& a, void* stream);
