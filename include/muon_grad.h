@@ -18,9 +18,11 @@
  *             w <- w - lr ((m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + weight_decay decay w);
  *             param <- w, rounded to param's type.
  *   muon_step_clipped runs muon_step with M <- beta M + c G.
+ * muon_step_clipped runs muon_step with M <- beta M + c G.
  * The norm is a float in device memory, so clipping needs no transfer to the host.  Where
  * several ranks own parts of the gradients, each takes its part's norm, the caller reduces
  * them (sum of squares, or maximum), and every rank clips by the reduced value.
+ * shampoo_step and muon_step_noalloc take no clip: scale their gradients in place first.
  *
  * Precision: the squares and sums of the L2 norm are 64-bit, in a fixed order (results are
  * bitwise reproducible), so no gradient is too small or too large for it; the norm is rounded
@@ -29,9 +31,9 @@
  * is rounded once.  Without a master that rounding loses updates below half a bf16 step.
  *
  * Lists: a list is laid out once (muon_grad_list_init, adamw_list_init: the tensors'
- * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used by any number of calls, as
- * long as the tensors stay where they are; their values may change.  The layout is enqueued
- * on the stream given (through kernel arguments: no host buffer, no copy, so it may be
+ * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used
+ * by any number of calls, as long as the tensors stay where they are; their values may
+ * change.  The layout is enqueued on the stream given (through kernel arguments: no host buffer, no copy, so it may be
  * captured); uses on another stream must be ordered after it by the caller.  Two calls in
  * flight at once need two lists.  A list is used on the device it was laid out on.
  */
@@ -115,6 +117,12 @@ int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm
 
 /* AdamW over the list.  hp as adamw_step; clip may be NULL (no clipping). */
 int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream);
+
+/* muon_step whose gradients are scaled by the coefficient of `clip` as the momentum reads
+ * them: M <- beta M + c G, in fp32, the gradients
+ * unchanged.  clip NULL is muon_step; MUON_EALIAS when clip->norm lies in a param or momentum. */
+int muon_step_clipped(const muon_matrix* mats, int32_t count, const muon_hparams* hp, const muon_clip* clip,
+                      void* workspace, size_t workspace_bytes, void* hip_stream);
 
 #ifdef __cplusplus
 }

@@ -138,6 +138,7 @@ _SIGNATURES = {
     "shampoo_workspace_size": (c_int, [_SMATP, c_int32, _SHPP, POINTER(c_size_t)]),
     "shampoo_step": (c_int, [_SMATP, c_int32, _SHPP, c_void_p, c_size_t, c_void_p]),
     "shampoo_plan_describe": (c_int, [_SMATP, c_int32, _SHPP, c_char_p, c_size_t]),
+    "muon_step_clipped": (c_int, [_MATP, c_int32, _HPP, POINTER(muon_clip), c_void_p, c_size_t, c_void_p]),
     "muon_grad_list_size": (c_int, [POINTER(muon_grad), c_int32, POINTER(c_size_t)]),
     "muon_grad_list_init": (c_int, [POINTER(muon_grad), c_int32, c_void_p, c_size_t, c_void_p, POINTER(muon_grad_list)]),
     "muon_grad_norm": (c_int, [POINTER(muon_grad_list), c_int32, c_void_p, c_void_p]),
@@ -433,9 +434,16 @@ class MuonStep:
     def cost(self) -> tuple[float, float]:
         return step_cost(self.arr, self.count, self.hp)
 
-    def __call__(self, stream=None) -> None:
-        step_raw(self.arr, self.count, self.hp, self.workspace.data_ptr(), self.workspace.numel(),
-                 _stream_handle(stream, self.device))
+    def __call__(self, stream=None, *, clip=None) -> None:
+        """One step; clip = (norm, max_norm) scales the gradients by min(1, max_norm / (norm + 1e-6))
+        as they are read (``muon_step_clipped``), with a float32 device tensor for the norm."""
+        if clip is None:
+            step_raw(self.arr, self.count, self.hp, self.workspace.data_ptr(), self.workspace.numel(),
+                     _stream_handle(stream, self.device))
+            return
+        _check(lib().muon_step_clipped(self.arr, self.count, ctypes.byref(self.hp), _clip_arg(clip, self.device),
+                                       c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
+                                       _stream_handle(stream, self.device)))
 
     def check(self, stream=None) -> None:
         """Raise MuonError if the last step reported a failure (muon_workspace_check)."""
@@ -486,8 +494,9 @@ def noalloc_check(stream=None, device=None) -> None:
     _check(lib().muon_workspace_check(None, 0, _stream_handle(stream, dev)))
 
 
-def muon_step(params, grads, moms, *, stream=None, **hp) -> None:
-    """One Muon step over lists of device tensors (param and momentum updated in place).
+def muon_step(params, grads, moms, *, stream=None, clip=None, **hp) -> None:
+    """One Muon step over lists of device tensors (param and momentum updated in place);
+    clip as in MuonStep.
 
     The throwaway workspace is allocated on the stream the step runs on, so the caching
     allocator does not hand its block to other work before that stream has finished with it.
@@ -501,7 +510,7 @@ def muon_step(params, grads, moms, *, stream=None, **hp) -> None:
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     with torch.cuda.stream(s):
         step = MuonStep(params, grads, moms, **hp)
-    step(s)
+    step(s, clip=clip)
 
 
 def adamw_step(p, g, m, v, *, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1,
@@ -779,6 +788,19 @@ def adamw_array(params, grads, ms, vs, masters=None, decays=None):
     return arr
 
 
+def _norm_arg(norm, device):
+    import torch
+
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != device:
+        raise ValueError(f"norm must be one float32 value on {device}")
+    return c_void_p(norm.data_ptr())
+
+
+def _clip_arg(clip, device):
+    norm, max_norm = clip
+    return ctypes.byref(muon_clip(_norm_arg(norm, device), float(max_norm), 0))
+
+
 class _List:
     """A list of tensors laid out on one device: what GradClip and AdamWStep share."""
 
@@ -826,17 +848,6 @@ class _List:
             with torch.cuda.device(self.device):
                 _check(fn(self._list, *args, c_void_p(s.cuda_stream)))
 
-    def _norm_arg(self, norm):
-        import torch
-
-        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.device:
-            raise ValueError(f"norm must be one float32 value on {self.device}")
-        return c_void_p(norm.data_ptr())
-
-    def _clip_arg(self, clip):
-        norm, max_norm = clip
-        return ctypes.byref(muon_clip(self._norm_arg(norm), float(max_norm), 0))
-
 
 class GradClip(_List):
     """A list of gradients laid out once, for their global norm and clipping by it.
@@ -857,7 +868,9 @@ class GradClip(_List):
 
         if out is not None:
             return out
-        with torch.cuda.stream(None if stream is None else self._stream(stream)):
+        if stream is None:
+            return torch.empty((), dtype=torch.float32, device=self.device)
+        with torch.cuda.stream(self._stream(stream)):
             return torch.empty((), dtype=torch.float32, device=self.device)
 
     def norm(self, kind="l2", *, out=None, stream=None):
@@ -865,19 +878,19 @@ class GradClip(_List):
         belongs to the stream of the call)."""
         code = _norm_kind(kind)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_norm, (code, self._norm_arg(out)), stream)
+        self._call(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream)
         return out
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
         """Scale the gradients in place by min(1, max_norm / (norm + 1e-6)); `norm` is a float32
         device tensor, for example one that was reduced over ranks."""
-        self._call(lib().muon_grad_clip, (self._clip_arg((norm, max_norm)),), stream)
+        self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream)
 
     def clip_norm(self, max_norm, kind="l2", *, out=None, stream=None):
         """norm(), then clip() by it; returns the norm from before."""
         code = _norm_kind(kind)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), self._norm_arg(out)), stream)
+        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream)
         return out
 
 
@@ -904,7 +917,7 @@ class AdamWStep(_List):
         self.hp.step = int(step)
         if lr is not None:
             self.hp.lr = float(lr)
-        arg = None if clip is None else self._clip_arg(clip)
+        arg = None if clip is None else _clip_arg(clip, self.device)
         self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream)
 
 

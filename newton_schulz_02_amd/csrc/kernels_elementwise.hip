@@ -2,7 +2,7 @@
 //   k_momentum  M <- beta*M + G (fp32 math, stored in M's dtype), per-tile partial sums of
 //               M'^2 (wave64 shuffle reduction), and the zero-padded row / transposed
 //               copies that the MFMA phase reads (transpose staged through LDS so both
-//               the read and the write are coalesced);
+//               the read and the write are coalesced); G may be scaled by a clip coefficient;
 //   k_norm      s = 1 / (sqrt(sum of partials) + eps) per matrix, summed in a fixed order
 //               (it also clears the contraction kernels' tail-split counters; the step's
 //               first momentum launch clears them and the workspace's status word too);
@@ -73,7 +73,9 @@ __device__ __forceinline__ void store_f32(float* p, const Chunk<S>& c) {
   for (int q = 0; q < Chunk<S>::N / 4; ++q) *(g_u32x4)(p + 4 * q) = *reinterpret_cast<const u32x4*>(f + 4 * q);
 }
 
-template <typename S>
+// CLIP: M' = beta*M + c*G, the product c*G rounded to fp32, with c from a norm on the device
+// (muon_step_clipped).
+template <typename S, bool CLIP>
 __global__ __launch_bounds__(256) void k_momentum(MomArgs a) {
   constexpr int CH = 16 / sizeof(S);  // elements per 16-byte chunk
   constexpr int CPR = kEwTile / CH;   // chunks per tile row
@@ -100,6 +102,8 @@ __global__ __launch_bounds__(256) void k_momentum(MomArgs a) {
   S* M = static_cast<S*>(d.mom);
   S* copy = static_cast<S*>(d.copy_out);
   const float beta = a.beta;
+  const float coef = CLIP ? clip_coef(a.clip) : 1.0f;
+  auto scaled = [coef](float g) { return CLIP ? coef * g : g; };
   const int tid = threadIdx.x;
   const int lr = tid / CPR;
   const int lc = (tid % CPR) * CH;
@@ -128,13 +132,13 @@ __global__ __launch_bounds__(256) void k_momentum(MomArgs a) {
         load_chunk(G + base, gv);
         load_chunk(M + base, mv);
 #pragma unroll
-        for (int e = 0; e < CH; ++e) st_f(&out.v[e], fmaf(beta, as_f(mv.v[e]), as_f(gv.v[e])));
+        for (int e = 0; e < CH; ++e) st_f(&out.v[e], fmaf(beta, as_f(mv.v[e]), scaled(as_f(gv.v[e]))));
         store_chunk(M + base, out);
       } else {
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
           if (gj + e < c) {
-            st_f(&out.v[e], fmaf(beta, ld_f(M + base + e), ld_f(G + base + e)));
+            st_f(&out.v[e], fmaf(beta, ld_f(M + base + e), scaled(ld_f(G + base + e))));
             M[base + e] = out.v[e];
           } else {
             st_f(&out.v[e], 0.0f);
@@ -238,10 +242,9 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 int muon_launch_momentum(const MomArgs& a, int dtype, void* stream) {
   if (a.total_tiles <= 0) return hipSuccess;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (dtype == kBF16)
-    hipLaunchKernelGGL(k_momentum<uint16_t>, dim3(a.total_tiles), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL(k_momentum<float>, dim3(a.total_tiles), dim3(256), 0, s, a);
+  const auto kernel = dtype == kBF16 ? (a.clip.norm ? k_momentum<uint16_t, true> : k_momentum<uint16_t, false>)
+                                     : (a.clip.norm ? k_momentum<float, true> : k_momentum<float, false>);
+  hipLaunchKernelGGL(kernel, dim3(a.total_tiles), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

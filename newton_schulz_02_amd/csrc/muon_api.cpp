@@ -183,7 +183,7 @@ int timed(int dev, hipStream_t s, const char* name, double flops, double bytes, 
 
 // Enqueue one launch of the plan on stream s.  Caller holds g_mu.
 int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, int cfg, char* ws,
-               const muon_hparams* hp, int count) {
+               const muon_hparams* hp, int count, ClipArg clip = {nullptr, 0.0f}) {
   const MatDesc* ddesc = reinterpret_cast<const MatDesc*>(ws + plan.desc_off);
   float* scale = reinterpret_cast<float*>(ws + plan.scale_off);
   float* partials = reinterpret_cast<float*>(ws + plan.partial_off);
@@ -202,6 +202,7 @@ int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, in
     a.tile_begin = int32_t(plan.mats[L.first].mom_prefix);
     a.total_tiles = int32_t(L.tiles);
     a.beta = hp->beta;
+    a.clip = clip;
     return timed(dev, s, L.dtype == kBF16 ? "momentum_bf16" : "momentum_f32", 0.0, L.bytes,
                  [&] { return muon_launch_momentum(a, L.dtype, s); });
   }
@@ -256,6 +257,25 @@ int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, in
                  [&] { return muon_launch_gemm_small(a, L.dtype, s); });
   return timed(dev, s, bf ? "gemm_bf16" : "gemm_f32", L.flops, 0.0,
                [&] { return muon_launch_gemm(a, L.dtype, s); });
+}
+
+int check_max_norm(float max_norm) {
+  if (!std::isfinite(max_norm) || max_norm < 0.0f) return fail(MUON_EINVAL, "max_norm is not finite and >= 0");
+  return MUON_OK;
+}
+
+int check_norm(const float* norm) {
+  if (!norm) return fail(MUON_EINVAL, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(MUON_EINVAL, "norm is not 4-byte aligned");
+  return MUON_OK;
+}
+
+int check_clip(const muon_clip* clip) {
+  int rc;
+  if (!clip) return fail(MUON_EINVAL, "clip is NULL");
+  if (clip->reserved != 0) return fail(MUON_EINVAL, "clip: reserved field must be 0");
+  if ((rc = check_norm(clip->norm)) != MUON_OK) return rc;
+  return check_max_norm(clip->max_norm);
 }
 
 // Validate, plan (with the tuned kernel choices) and upload the descriptors.  Caller holds
@@ -356,8 +376,9 @@ int muon_plan_describe(const muon_matrix* mats, int32_t count, const muon_hparam
   }
 }
 
-int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, void* workspace,
-              size_t workspace_bytes, void* hip_stream) {
+namespace {
+int run_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, ClipArg clip, void* workspace,
+             size_t workspace_bytes, void* hip_stream) {
   try {
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
@@ -367,13 +388,36 @@ int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, vo
     if (rc != MUON_OK || count == 0) return rc;
     char* ws = static_cast<char*>(workspace);
     for (const PlanLaunch& L : plan.launches) {
-      rc = run_launch(dev, s, plan, L, L.cfg, ws, hp, count);
+      rc = run_launch(dev, s, plan, L, L.cfg, ws, hp, count, clip);
       if (rc != MUON_OK) return rc;
     }
     return MUON_OK;
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }
+}
+}  // namespace
+
+int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, void* workspace,
+              size_t workspace_bytes, void* hip_stream) {
+  return run_step(mats, count, hp, {nullptr, 0.0f}, workspace, workspace_bytes, hip_stream);
+}
+
+int muon_step_clipped(const muon_matrix* mats, int32_t count, const muon_hparams* hp, const muon_clip* clip,
+                      void* workspace, size_t workspace_bytes, void* hip_stream) {
+  if (!clip) return run_step(mats, count, hp, {nullptr, 0.0f}, workspace, workspace_bytes, hip_stream);
+  const int rc = check_clip(clip);
+  if (rc != MUON_OK) return rc;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(clip->norm);
+  for (int32_t i = 0; mats && i < count; ++i) {
+    const muon_matrix& x = mats[i];
+    if (x.rows < 1 || x.cols < 1 || x.rows >= (int64_t(1) << 31) || x.cols >= (int64_t(1) << 31)) continue;  // refused below
+    const uintptr_t bytes = uintptr_t(x.rows) * uintptr_t(x.cols) * (x.dtype == MUON_BF16 ? 2 : 4);
+    for (const uintptr_t out : {reinterpret_cast<uintptr_t>(x.param), reinterpret_cast<uintptr_t>(x.momentum)})
+      if (at + 4 > out && at < out + bytes)
+        return fail(MUON_EALIAS, "clip: norm lies in an output of matrix " + std::to_string(i));
+  }
+  return run_step(mats, count, hp, {clip->norm, clip->max_norm}, workspace, workspace_bytes, hip_stream);
 }
 
 namespace {
@@ -942,25 +986,6 @@ int on_list_device(const ListHandle& h, int* dev) {
     return fail(MUON_EINVAL, "the list was laid out on device " + std::to_string(h.device) + ", the current one is " +
                                  std::to_string(*dev));
   return check_device(*dev);
-}
-
-int check_max_norm(float max_norm) {
-  if (!std::isfinite(max_norm) || max_norm < 0.0f) return fail(MUON_EINVAL, "max_norm is not finite and >= 0");
-  return MUON_OK;
-}
-
-int check_norm(const float* norm) {
-  if (!norm) return fail(MUON_EINVAL, "norm is NULL");
-  if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(MUON_EINVAL, "norm is not 4-byte aligned");
-  return MUON_OK;
-}
-
-int check_clip(const muon_clip* clip) {
-  int rc;
-  if (!clip) return fail(MUON_EINVAL, "clip is NULL");
-  if (clip->reserved != 0) return fail(MUON_EINVAL, "clip: reserved field must be 0");
-  if ((rc = check_norm(clip->norm)) != MUON_OK) return rc;
-  return check_max_norm(clip->max_norm);
 }
 
 int check_kind(int32_t kind) {

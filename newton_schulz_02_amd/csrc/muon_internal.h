@@ -141,6 +141,12 @@ struct GemmArgs {
   int32_t split_spins;   // polls of a last piece's bounded wait (kSplitSpins)
 };
 
+// Where a clip coefficient comes from; norm null: none (1).
+struct ClipArg {
+  const float* norm;
+  float max_norm;
+};
+
 struct MomArgs {
   const MatDesc* desc;
   float* partials;       // one partial sum of squares per momentum tile
@@ -153,6 +159,7 @@ struct MomArgs {
   int32_t tile_begin;    // mom_prefix of `first`
   int32_t total_tiles;   // tiles of the range
   float beta;
+  ClipArg clip;          // what G is scaled by as it is read
 };
 
 struct NormArgs {
@@ -204,12 +211,6 @@ struct AdamRec {
   uint16_t param_bf16, grad_bf16;
   float decay;
   uint32_t reserved;
-};
-
-// Where a clip coefficient comes from; norm null: none (1).
-struct ClipArg {
-  const float* norm;
-  float max_norm;
 };
 
 struct GradArgs {

@@ -153,6 +153,30 @@ def test_valid_layout_without_gpu_reports_hip_error():
                                         ctypes.byref(lst)) == nm.MUON_EHIP
 
 
+def test_clipped_muon_step_refusals():
+    from tests.test_abi import HP, mats
+
+    def run(norm=1 << 30, max_norm=1.0, reserved=0, arr=None):
+        clip = nm.muon_clip(norm, max_norm, reserved)
+        return nm.lib().muon_step_clipped(arr or mats((8, 8), (8, 16)), 2, ctypes.byref(HP), ctypes.byref(clip),
+                                          ctypes.c_void_p(1 << 32), 1 << 40, None)
+
+    a = mats((8, 8), (8, 16))
+    assert run(norm=0) == nm.MUON_EINVAL and run(norm=(1 << 30) + 2) == nm.MUON_EINVAL
+    assert run(max_norm=-1.0) == nm.MUON_EINVAL and run(max_norm=math.inf) == nm.MUON_EINVAL
+    assert run(max_norm=math.nan) == nm.MUON_EINVAL and run(reserved=1) == nm.MUON_EINVAL
+    for out, n in ((a[0].param, 8 * 8 * 2), (a[1].momentum, 8 * 16 * 2)):
+        assert run(norm=out) == nm.MUON_EALIAS and run(norm=out + n - 4) == nm.MUON_EALIAS
+    if not _gpu_visible():  # just outside: valid, and stops at the first HIP call
+        assert run(norm=a[0].param - 4) == nm.MUON_EHIP and run(norm=a[0].param + 8 * 8 * 2) == nm.MUON_EHIP
+    bad = mats((8, 8), (8, 16))
+    bad[1].rows = -1
+    assert run(arr=bad) == nm.MUON_EINVAL
+    # No clip: muon_step's own refusals.
+    assert nm.lib().muon_step_clipped(bad, 2, ctypes.byref(HP), None, ctypes.c_void_p(1 << 32), 1 << 40,
+                                      None) == nm.MUON_EINVAL
+
+
 def test_binding_refusals():
     b, f, h = (torch.zeros(4, 6, dtype=t) for t in (torch.bfloat16, torch.float32, torch.float16))
     with pytest.raises(ValueError, match="contiguous"):
