@@ -120,16 +120,25 @@ __device__ __forceinline__ Piece<S, BYTES> piece_of(const GradRec& r, uint32_t c
   return x;
 }
 
-// f(vector) for each of this thread's vectors of a piece; STORE: write them back.  A whole
-// piece has all its loads in flight before the first vector is used; else vectors that reach
-// outside go element by element (with zeros for what is outside, which change neither a sum
-// nor a maximum).
+// The elements of [lo, hi) that no whole vector of n elements covers, up to n - 1 at each end:
+// one per thread, -1 for a thread without one.
+__device__ __forceinline__ int edge_of(int lo, int hi, int n) {
+  const int head = min(hi, (lo + n - 1) / n * n), tail = max(head, hi / n * n);
+  const int i = lo + int(threadIdx.x);
+  if (i < head) return i;
+  return i - head + tail < hi ? i - head + tail : -1;
+}
+
+// f on each of this thread's vectors of a piece (and on single elements at the ends of one that
+// is not whole); STORE: write them back.  All loads are in flight before the first use, in a
+// piece that is not whole, too: one vector after the other there, the norm of 23 ragged
+// tensors took 10 us, now NEW.
 template <bool STORE, typename S, int BYTES, typename F>
 __device__ __forceinline__ void each_vec(const Piece<S, BYTES>& x, F&& f) {
   constexpr int N = Vec<S>::N, U = BYTES / (256 * 16);
   const int tid = threadIdx.x;
+  Vec<S> v[U];
   if (x.lo == 0 && x.hi == x.kAll) {
-    Vec<S> v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) v[u].load(x.p + (u * 256 + tid) * N);
 #pragma unroll
@@ -139,34 +148,40 @@ __device__ __forceinline__ void each_vec(const Piece<S, BYTES>& x, F&& f) {
     }
     return;
   }
-  for (int i = tid * N; i < x.hi; i += 256 * N) {
-    Vec<S> v;
-    if (i >= x.lo && i + N <= x.hi) {
-      v.load(x.p + i);
-      f(v);
-      if (STORE) v.store(x.p + i);
-      continue;
-    }
-    float e[N];
+  if (x.hi <= x.lo) return;
+  const int at = edge_of(x.lo, x.hi, N);
+  float edge = at >= 0 ? ld_f(x.p + at) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) e[k] = i + k >= x.lo && i + k < x.hi ? ld_f(x.p + i + k) : 0.0f;
-    v.set(e);
-    f(v);
-    if (STORE) {
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 256 + tid) * N;
+    v[u].v = 0;  // zeros change neither a sum nor a maximum
+    if (i >= x.lo && i + N <= x.hi) v[u].load(x.p + i);
+  }
+  f(edge);
+  if (STORE && at >= 0) st_f(x.p + at, edge);
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (i + k >= x.lo && i + k < x.hi) st_f(x.p + i + k, v.get(k));
-    }
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 256 + tid) * N;
+    f(v[u]);
+    if (STORE && i >= x.lo && i + N <= x.hi) v[u].store(x.p + i);
   }
 }
 
 template <bool INF>
+struct Take {
+  Part& part;
+  template <typename S>
+  __device__ __forceinline__ void operator()(const Vec<S>& v) {
+#pragma unroll
+    for (int e = 0; e < Vec<S>::N; ++e) part.template take<INF>(v.get(e), e);
+  }
+  __device__ __forceinline__ void operator()(float g) { part.template take<INF>(g, 0); }
+};
+
+template <bool INF>
 __device__ __forceinline__ Part norm_chunks(const GradArgs& a) {
   Part part;
-  auto take = [&](const auto& v) {
-#pragma unroll
-    for (int e = 0; e < std::decay_t<decltype(v)>::N; ++e) part.template take<INF>(v.get(e), e);
-  };
+  Take<INF> take{part};
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const GradRec r = a.recs[a.map[c]];
     if (r.dtype == kBF16) each_vec<false>(piece_of<uint16_t, kGradChunk>(r, c), take);
@@ -191,8 +206,8 @@ __device__ __forceinline__ double reduce(double x, bool inf, double* red) {
 // complete (s_waitcnt) before its workgroup counts itself.  No device-wide release: it writes
 // back a whole L2, and one per workgroup took 36 us over 1024 workgroups.  Counts of one
 // address are made one after another (10 ns each), so a workgroup counts itself among those
-// with its index modulo kTickets, and the last of each of these among the last ones.  All
-// counts are back at 0 at the end.
+// with its index modulo kTickets, and the last of each of these among the last ones; up to 64
+// workgroups count themselves at once.  All counts are back at 0 at the end.
 __device__ __forceinline__ uint32_t count_self(uint32_t* ticket) {
   return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -207,14 +222,19 @@ __global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
     if (threadIdx.x == 0) {
       __hip_atomic_store(a.parts + blockIdx.x, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __builtin_amdgcn_s_waitcnt(0);
-      const unsigned mine = blockIdx.x % kTickets;
-      uint32_t* ticket = a.tickets + (1 + mine) * (kLine / 4);
-      last = count_self(ticket) == (grid - mine - 1) / kTickets;
-      if (last) {
-        __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = count_self(a.tickets) == min(grid, unsigned(kTickets)) - 1;
-        if (last) __hip_atomic_store(a.tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const bool few = grid <= 64;
+      bool done = true;
+      if (!few) {
+        const unsigned mine = blockIdx.x % kTickets;
+        uint32_t* ticket = a.tickets + (1 + mine) * (kLine / 4);
+        done = count_self(ticket) == (grid - mine - 1) / kTickets;
+        if (done) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+      if (done) {
+        done = count_self(a.tickets) == (few ? grid : unsigned(kTickets)) - 1;
+        if (done) __hip_atomic_store(a.tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      last = done;
     }
     __syncthreads();
     if (!last) return;
@@ -226,18 +246,22 @@ __global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
   if (threadIdx.x == 0) *a.norm = inf ? __uint_as_float(uint32_t(x)) : float(sqrt(x));
 }
 
-template <typename S>
-__device__ __forceinline__ void scale_vec(Vec<S>& x, float coef) {
-  float f[Vec<S>::N];
+struct Scale {
+  float coef;
+  template <typename S>
+  __device__ __forceinline__ void operator()(Vec<S>& v) {
+    float f[Vec<S>::N];
 #pragma unroll
-  for (int e = 0; e < Vec<S>::N; ++e) f[e] = coef * x.get(e);
-  x.set(f);
-}
+    for (int e = 0; e < Vec<S>::N; ++e) f[e] = coef * v.get(e);
+    v.set(f);
+  }
+  __device__ __forceinline__ void operator()(float& g) { g *= coef; }
+};
 
 __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
   const float coef = clip_coef(a.clip);
   if (coef == 1.0f) return;
-  auto scale = [=](auto& v) { scale_vec(v, coef); };
+  Scale scale{coef};
   // By half chunks (512 small fp32 matrices, 1.4 GB: 450 us by 16 KiB, 475 by 32 KiB and by
   // 8 KiB), a workgroup each, and backwards, since what the norm read last may still be in the
   // memory-side cache (1 % of a layer's clipping).
@@ -277,18 +301,6 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
   for (int k = 0; k < 4; ++k) v[k] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(f[k]));
   __builtin_nontemporal_store(__builtin_bit_cast(u32x2, v), (__attribute__((address_space(1))) u32x2_at2*)(p));
 }
-template <typename S>
-__device__ __forceinline__ void load_some(const S* p, float (&f)[4], int i, int lo, int hi) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) f[k] = i + k >= lo && i + k < hi ? ld_f(p + i + k) : 0.0f;
-}
-template <typename S>
-__device__ __forceinline__ void store_some(S* p, const float (&f)[4], int i, int lo, int hi) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (i + k >= lo && i + k < hi) st_f(p + i + k, f[k]);
-}
-
 // The elements of chunk c of one tensor; a master takes the place of the param as what is
 // updated.  Chunks start where m lies on a line boundary, so buffers that lie alike (those of
 // one flat bucket per type) are all read and written by whole lines.
@@ -308,8 +320,8 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
   const float wd = a.wd * r.decay;
   const int tid = threadIdx.x;
   constexpr int U = int(kAdamChunk) / 1024;
+  float xs[U][4], gs[U][4], ms[U][4], vs[U][4];
   if (at >= 0 && r.n - at >= kAdamChunk) {
-    float xs[U][4], gs[U][4], ms[U][4], vs[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = (u * 256 + tid) * 4;
@@ -330,36 +342,44 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
     }
     return;
   }
+  // The first or last chunk of a tensor: vectors inside it, and up to three single elements at
+  // each end.
   const int lo = at < 0 ? int(-at) : 0;
   const int hi = int(min(kAdamChunk, r.n - at));
-  for (int i = tid * 4; i < hi; i += 1024) {
-    if (i + 4 <= lo) continue;
-    const bool all = i >= lo && i + 4 <= hi;
-    float xs[4], gs[4], ms[4], vs[4];
-    if (all) {
-      load4(x + i, xs);
-      load4(g + i, gs);
-      load4(m + i, ms);
-      load4(v + i, vs);
-    } else {
-      load_some(x, xs, i, lo, hi);
-      load_some(g, gs, i, lo, hi);
-      load_some(m, ms, i, lo, hi);
-      load_some(v, vs, i, lo, hi);
-    }
+  const int e = edge_of(lo, hi, 4);
+  float xe = 0.0f, ge = 0.0f, me = 0.0f, ve = 0.0f;
+  if (e >= 0) {
+    xe = ld_f(x + e);
+    ge = ld_f(g + e);
+    me = m[e];
+    ve = v[e];
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) adamw_one(xs[k], coef * gs[k], ms[k], vs[k], a, wd);
-    if (all) {
-      store4(m + i, ms);
-      store4(v + i, vs);
-      store4(x + i, xs);
-      if (MASTER) store4(p + i, xs);
-    } else {
-      store_some(m, ms, i, lo, hi);
-      store_some(v, vs, i, lo, hi);
-      store_some(x, xs, i, lo, hi);
-      if (MASTER) store_some(p, xs, i, lo, hi);
-    }
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 256 + tid) * 4;
+    if (i < lo || i + 4 > hi) continue;
+    load4(x + i, xs[u]);
+    load4(g + i, gs[u]);
+    load4(m + i, ms[u]);
+    load4(v + i, vs[u]);
+  }
+  if (e >= 0) {
+    adamw_one(xe, coef * ge, me, ve, a, wd);
+    m[e] = me;
+    v[e] = ve;
+    st_f(x + e, xe);
+    if (MASTER) st_f(p + e, xe);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = (u * 256 + tid) * 4;
+    if (i < lo || i + 4 > hi) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, wd);
+    store4(m + i, ms[u]);
+    store4(v + i, vs[u]);
+    store4(x + i, xs[u]);
+    if (MASTER) store4(p + i, xs[u]);
   }
 }
 
