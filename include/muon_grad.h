@@ -97,8 +97,8 @@ int adamw_list_size(const adamw_tensor* tensors, int32_t count, size_t* bytes);
 
 /* Lay out a list in `workspace` (device memory of at least the size above, 256-byte aligned,
  * owned by the caller, kept as long as the list is used and written by nothing else) and fill
- * *list.  count == 0 is a list of no tensors (its norm is 0).  Errors as the size calls, and
- * MUON_ENOSPC. */
+ * *list.  count == 0 is a list of no tensors (its norm is 0).  Errors as the size calls,
+ * MUON_ENOSPC, and MUON_EALIAS when the workspace overlaps a tensor of the list. */
 int muon_grad_list_init(const muon_grad* grads, int32_t count, void* workspace, size_t workspace_bytes,
                         void* hip_stream, muon_grad_list* list);
 int adamw_list_init(const adamw_tensor* tensors, int32_t count, void* workspace, size_t workspace_bytes,

@@ -10,12 +10,6 @@ namespace muon {
 
 namespace {
 
-struct Span {
-  uintptr_t lo, hi;
-  int32_t tensor;
-  bool output;
-};
-
 int refuse(std::string* err, int status, int32_t i, const char* what) {
   char buf[160];
   snprintf(buf, sizeof buf, "tensor %d: %s", i, what);
@@ -24,11 +18,11 @@ int refuse(std::string* err, int status, int32_t i, const char* what) {
 }
 
 // No output may overlap another output or any gradient (which may overlap each other).
-int check_spans(std::vector<Span>& spans, std::string* err) {
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+int check_spans(std::vector<ListSpan>& spans, std::string* err) {
+  std::sort(spans.begin(), spans.end(), [](const ListSpan& a, const ListSpan& b) { return a.lo < b.lo; });
   uintptr_t out_hi = 0, in_hi = 0;
   int32_t out_t = -1, in_t = -1;
-  for (const Span& s : spans) {
+  for (const ListSpan& s : spans) {
     const bool hits_out = s.lo < out_hi, hits_in = s.output && s.lo < in_hi;
     if (hits_out || hits_in) {
       char buf[160];
@@ -75,7 +69,6 @@ int check_count(const void* list, int32_t count, std::string* err) {
 int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::string* err) {
   int rc = check_count(grads, count, err);
   if (rc != MUON_OK) return rc;
-  std::vector<Span> spans;
   std::vector<GradRec> recs;
   uint64_t chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
@@ -89,7 +82,7 @@ int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::st
     if (!p) return refuse(err, MUON_EINVAL, i, "NULL pointer");
     if (p % uintptr_t(es)) return refuse(err, MUON_EINVAL, i, "pointer not aligned to its element size");
     if (uintptr_t(x.n) * uintptr_t(es) > UINTPTR_MAX - p) return refuse(err, MUON_EINVAL, i, "buffer passes the end of memory");
-    spans.push_back({p, p + uintptr_t(x.n) * uintptr_t(es), i, true});
+    t->spans.push_back({p, p + uintptr_t(x.n) * uintptr_t(es), i, true});
     recs.push_back({uint64_t(p), x.n, uint32_t(chunks), uint32_t(x.dtype)});
     // Chunks start on line boundaries, the first one at or before the tensor.
     chunks += uint64_t(ceil_div(x.n * es + int64_t(p % uintptr_t(kLine)), kGradChunk));
@@ -97,7 +90,7 @@ int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::st
     t->read_bytes += double(x.n) * es;
   }
   t->write_bytes = t->read_bytes;
-  if ((rc = check_spans(spans, err)) != MUON_OK) return rc;
+  if ((rc = check_spans(t->spans, err)) != MUON_OK) return rc;
   t->chunks = uint32_t(chunks);
   lay_out(recs, t);
   t->ws_bytes += kNormParts * sizeof(double);
@@ -107,7 +100,6 @@ int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::st
 int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, std::string* err) {
   int rc = check_count(tensors, count, err);
   if (rc != MUON_OK) return rc;
-  std::vector<Span> spans;
   std::vector<AdamRec> recs;
   uint64_t chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
@@ -133,7 +125,7 @@ int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, s
       if (!b.p) continue;
       if (b.p % uintptr_t(b.es)) return refuse(err, MUON_EINVAL, i, "pointer not aligned to its element size");
       if (uintptr_t(x.n) * uintptr_t(b.es) > UINTPTR_MAX - b.p) return refuse(err, MUON_EINVAL, i, "buffer passes the end of memory");
-      spans.push_back({b.p, b.p + uintptr_t(x.n) * uintptr_t(b.es), i, b.output});
+      t->spans.push_back({b.p, b.p + uintptr_t(x.n) * uintptr_t(b.es), i, b.output});
       // A master takes the param's place as what is read.
       if (!(x.master && b.p == uintptr_t(x.param))) t->read_bytes += double(x.n) * b.es;
       if (b.output) t->write_bytes += double(x.n) * b.es;
@@ -155,9 +147,16 @@ int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, s
     chunks += uint64_t(ceil_div(x.n + int64_t(r.m % uint64_t(kLine) / 4), kAdamChunk));
     t->elems += x.n;
   }
-  if ((rc = check_spans(spans, err)) != MUON_OK) return rc;
+  if ((rc = check_spans(t->spans, err)) != MUON_OK) return rc;
   t->chunks = uint32_t(chunks);
   lay_out(recs, t);
+  return MUON_OK;
+}
+
+int check_list_workspace(const ListTable& t, const void* workspace, std::string* err) {
+  const uintptr_t lo = uintptr_t(workspace), hi = lo + t.ws_bytes;
+  for (const ListSpan& s : t.spans)
+    if (s.lo < hi && lo < s.hi) return refuse(err, MUON_EALIAS, s.tensor, "the workspace overlaps a buffer");
   return MUON_OK;
 }
 

@@ -20,7 +20,15 @@ namespace muon {
 constexpr int32_t kMaxList = 1 << 20;              // tensors in one list
 constexpr int64_t kMaxListElems = int64_t(1) << 40;  // elements in one list
 
+// A buffer of a list's tensor; no output may overlap another output or any gradient.
+struct ListSpan {
+  uintptr_t lo, hi;
+  int32_t tensor;
+  bool output;
+};
+
 struct ListTable {
+  std::vector<ListSpan> spans;  // in order of address
   std::vector<uint32_t> words;  // head and entries, as uploaded
   uint32_t chunks = 0;
   int32_t entries = 0;          // tensors that are not empty
@@ -34,6 +42,9 @@ struct ListTable {
 // Validate a list and lay out its table.  MUON_OK, or a status with the reason in *err.
 int build_grad_list(const muon_grad* grads, int32_t count, ListTable* t, std::string* err);
 int build_adamw_list(const adamw_tensor* tensors, int32_t count, ListTable* t, std::string* err);
+
+// MUON_EALIAS when the list's workspace overlaps one of its buffers.
+int check_list_workspace(const ListTable& t, const void* workspace, std::string* err);
 
 // What a muon_grad_list / adamw_list holds.
 struct ListHandle {

@@ -942,6 +942,9 @@ int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t worksp
   if (workspace_bytes < t.ws_bytes)
     return fail(MUON_ENOSPC, "workspace has " + std::to_string(workspace_bytes) + " bytes, needs " +
                                  std::to_string(t.ws_bytes));
+  std::string err;
+  const int alias = check_list_workspace(t, workspace, &err);
+  if (alias != MUON_OK) return fail(alias, err);
   std::lock_guard<std::mutex> lock(g_mu);
   ListHandle h;
   std::memset(&h, 0, sizeof h);

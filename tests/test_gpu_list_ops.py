@@ -164,6 +164,19 @@ def test_clip_by_a_norm_in_hand_and_one_shot_forms():
     assert guards_whole(bufs)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_clip_into_denormals(dtype):
+    """Products below the normal range keep the type's denormals (c itself is normal)."""
+    log(f"clip into denormals {dtype}")
+    views, bufs = make([(5001, dtype), (40000, dtype)], 12, 1, std=1e-30)
+    host = [to64(v) for v in views]
+    nm.GradClip(views).clip(torch.tensor(1e10, device=DEV), 1.0)
+    for v, w in zip(views, clip_grads(host, 1e10, 1.0)):
+        assert np.all(np.abs(to64(v) - w) <= clip_bound(w, v.dtype))
+        assert 0 < np.abs(to64(v)).max() < 2.0 ** -126
+    assert guards_whole(bufs)
+
+
 def test_a_norm_below_the_limit_leaves_every_bit():
     log("clip below the limit")
     views, _ = make(LISTS["many"], 9)

@@ -56,7 +56,7 @@ def test_grad_list_refusals(mutate, code):
     mutate(arr)
     assert size_of("muon_grad_list_size", arr, 2)[0] == code
     lst = nm.muon_grad_list()
-    assert nm.lib().muon_grad_list_init(arr, 2, ctypes.c_void_p(BASE), 1 << 30, None, ctypes.byref(lst)) == code
+    assert nm.lib().muon_grad_list_init(arr, 2, ctypes.c_void_p(1 << 32), 1 << 30, None, ctypes.byref(lst)) == code
     assert nm.last_error()
 
 
@@ -82,7 +82,7 @@ def test_adamw_list_refusals(mutate, code):
     mutate(arr)
     assert size_of("adamw_list_size", arr, 2)[0] == code
     lst = nm.adamw_list()
-    assert nm.lib().adamw_list_init(arr, 2, ctypes.c_void_p(BASE), 1 << 30, None, ctypes.byref(lst)) == code
+    assert nm.lib().adamw_list_init(arr, 2, ctypes.c_void_p(1 << 32), 1 << 30, None, ctypes.byref(lst)) == code
 
 
 def test_shared_gradients_of_adamw_and_empty_tensors_are_allowed():
@@ -123,8 +123,16 @@ def test_workspace_refusals():
     init = nm.lib().muon_grad_list_init
     assert init(arr, 1, None, need, None, ctypes.byref(lst)) == nm.MUON_EINVAL
     assert init(arr, 1, ctypes.c_void_p(BASE + 64), need, None, ctypes.byref(lst)) == nm.MUON_EINVAL
-    assert init(arr, 1, ctypes.c_void_p(BASE), need - 1, None, ctypes.byref(lst)) == nm.MUON_ENOSPC
-    assert init(arr, 1, ctypes.c_void_p(BASE), need, None, None) == nm.MUON_EINVAL
+    assert init(arr, 1, ctypes.c_void_p(1 << 32), need - 1, None, ctypes.byref(lst)) == nm.MUON_ENOSPC
+    assert init(arr, 1, ctypes.c_void_p(1 << 32), need, None, None) == nm.MUON_EINVAL
+    # A workspace that reaches into the tensor, or starts inside it.
+    for at in (BASE, (BASE - need) // 256 * 256 + 256):
+        assert init(arr, 1, ctypes.c_void_p(at), need, None, ctypes.byref(lst)) == nm.MUON_EALIAS
+    many = adamw(1 << 20)
+    need = size_of("adamw_list_size", many, 1)[1]
+    alist = nm.adamw_list()
+    assert nm.lib().adamw_list_init(many, 1, ctypes.c_void_p(many[0].v + 256), need, None,
+                                    ctypes.byref(alist)) == nm.MUON_EALIAS
 
 
 def test_calls_refuse_a_handle_that_no_init_filled():
@@ -149,7 +157,7 @@ def test_calls_refuse_a_handle_that_no_init_filled():
 def test_valid_layout_without_gpu_reports_hip_error():
     lst = nm.muon_grad_list()
     arr = grads(100)
-    assert nm.lib().muon_grad_list_init(arr, 1, ctypes.c_void_p(BASE), 1 << 20, None,
+    assert nm.lib().muon_grad_list_init(arr, 1, ctypes.c_void_p(1 << 32), 1 << 20, None,
                                         ctypes.byref(lst)) == nm.MUON_EHIP
 
 
