@@ -76,7 +76,7 @@ __device__ __forceinline__ void store_f32(float* p, const Chunk<S>& c) {
 // CLIP: M' = beta*M + c*G, the product c*G rounded to fp32, with c from a norm on the device
 // (muon_step_clipped).
 template <typename S, bool CLIP>
-__global__ __launch_bounds__(256) void k_momentum(MomArgs a) {
+__global__ __launch_bounds__(256) void k_momentum(MomArgs a, ClipArg clip) {
   constexpr int CH = 16 / sizeof(S);  // elements per 16-byte chunk
   constexpr int CPR = kEwTile / CH;   // chunks per tile row
   constexpr int RPP = 256 / CPR;      // tile rows per pass
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256) void k_momentum(MomArgs a) {
   S* M = static_cast<S*>(d.mom);
   S* copy = static_cast<S*>(d.copy_out);
   const float beta = a.beta;
-  const float coef = CLIP ? clip_coef(a.clip) : 1.0f;
+  const float coef = CLIP ? clip_coef(clip) : 1.0f;
   auto scaled = [coef](float g) { return CLIP ? coef * g : g; };
   const int tid = threadIdx.x;
   const int lr = tid / CPR;
@@ -242,9 +242,16 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
 int muon_launch_momentum(const MomArgs& a, int dtype, void* stream) {
   if (a.total_tiles <= 0) return hipSuccess;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const auto kernel = dtype == kBF16 ? (a.clip.norm ? k_momentum<uint16_t, true> : k_momentum<uint16_t, false>)
-                                     : (a.clip.norm ? k_momentum<float, true> : k_momentum<float, false>);
-  hipLaunchKernelGGL(kernel, dim3(a.total_tiles), dim3(256), 0, s, a);
+  const auto kernel = dtype == kBF16 ? k_momentum<uint16_t, false> : k_momentum<float, false>;
+  hipLaunchKernelGGL(kernel, dim3(a.total_tiles), dim3(256), 0, s, a, ClipArg{nullptr, 0.0f});
+  return hipGetLastError();
+}
+
+int muon_launch_momentum_clipped(const MomArgs& a, const ClipArg& clip, int dtype, void* stream) {
+  if (a.total_tiles <= 0) return hipSuccess;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const auto kernel = dtype == kBF16 ? k_momentum<uint16_t, true> : k_momentum<float, true>;
+  hipLaunchKernelGGL(kernel, dim3(a.total_tiles), dim3(256), 0, s, a, clip);
   return hipGetLastError();
 }
 

@@ -16,7 +16,6 @@
 #include <type_traits>
 
 #include "list_math.h"
-#include "muon_internal.h"
 
 using namespace muon;
 

@@ -4,7 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
-#include "muon_internal.h"
+#include "list_types.h"
 
 namespace muon {
 

@@ -13,7 +13,7 @@
 #include <vector>
 
 #include "../../include/muon_grad.h"
-#include "muon_internal.h"
+#include "list_types.h"
 
 namespace muon {
 

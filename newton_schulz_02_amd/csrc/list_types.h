@@ -1,0 +1,76 @@
+// Types shared by the host side and the kernels of the list operators (muon_grad.h) and of the
+// clipped Muon step.
+#pragma once
+
+#include <cstdint>
+
+#include "muon_internal.h"
+
+namespace muon {
+
+// Where a clip coefficient comes from; norm null: none (1).
+struct ClipArg {
+  const float* norm;
+  float max_norm;
+};
+
+constexpr int64_t kLine = 128;         // gradient chunks start on multiples of this address
+constexpr int kTickets = 8;            // groups in which a norm's workgroups count themselves
+constexpr int64_t kListTickets = 256;  // a list's workspace: status word, counts, entries
+constexpr int64_t kListHead = kListTickets + (kTickets + 1) * kLine;
+constexpr int64_t kGradChunk = 32768;  // bytes of one chunk of a gradient list
+// Elements of one chunk of an AdamW list: 2048 against 1024, us: bf16 param and gradient
+// 469 / 498, fp32 305 / 300, bf16 with master 1231 / 1201; 4096 is slower for all.
+constexpr int64_t kAdamChunk = 2048;
+// Most workgroups (and partial results) of a norm: a few long ones, each 32 KiB of loads ahead.
+// us of a 4096-hidden layer in bf16 / of 512 small fp32 matrices: 512 workgroups 61.5 / 200,
+// 768 63.4 / 205, 1024 64.1 / 207, 2048 69.8 / 223; 16 KiB chunks with 1024 63.4 / 204; 64 KiB
+// with 512 65.7 / 208.
+constexpr int kNormParts = 512;
+
+struct GradRec {
+  uint64_t ptr;
+  int64_t n;
+  uint32_t first;  // first chunk
+  uint32_t dtype;
+};
+
+struct AdamRec {
+  uint64_t param, grad, m, v, master;
+  int64_t n;
+  uint32_t first;  // first chunk
+  uint16_t param_bf16, grad_bf16;
+  float decay;
+  uint32_t reserved;
+};
+
+struct GradArgs {
+  const GradRec* recs;
+  const uint32_t* map;  // tensor of each chunk
+  uint32_t chunks;
+  double* parts;     // one per workgroup of the norm
+  uint32_t* tickets; // counts of the norm's workgroups that are done; 0 between launches
+  float* norm;     // output of the norm
+  int32_t inf;     // largest magnitude instead of L2
+  ClipArg clip;
+};
+
+struct AdamListArgs {
+  const AdamRec* recs;
+  const uint32_t* map;  // tensor of each chunk
+  uint32_t chunks;
+  ClipArg clip;
+  float lr, beta1, beta2, eps, wd;
+  float bc1, bc2;
+};
+
+}  // namespace muon
+
+// Kernel launchers (kernels_list.hip, kernels_elementwise.hip).  Each returns a hipError_t as int.
+int muon_launch_grad_map(const muon::GradRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream);
+int muon_launch_adamw_map(const muon::AdamRec* recs, int count, uint32_t chunks, uint32_t* map, void* stream);
+int muon_launch_grad_norm(const muon::GradArgs& a, void* stream);
+int muon_launch_grad_clip(const muon::GradArgs& a, void* stream);
+int muon_launch_adamw_list(const muon::AdamListArgs& a, void* stream);
+// muon_launch_momentum with G scaled by the coefficient of `clip` (its norm is not null).
+int muon_launch_momentum_clipped(const muon::MomArgs& a, const muon::ClipArg& clip, int dtype, void* stream);

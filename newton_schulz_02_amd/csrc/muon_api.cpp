@@ -202,9 +202,9 @@ int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, in
     a.tile_begin = int32_t(plan.mats[L.first].mom_prefix);
     a.total_tiles = int32_t(L.tiles);
     a.beta = hp->beta;
-    a.clip = clip;
-    return timed(dev, s, L.dtype == kBF16 ? "momentum_bf16" : "momentum_f32", 0.0, L.bytes,
-                 [&] { return muon_launch_momentum(a, L.dtype, s); });
+    return timed(dev, s, L.dtype == kBF16 ? "momentum_bf16" : "momentum_f32", 0.0, L.bytes, [&] {
+      return clip.norm ? muon_launch_momentum_clipped(a, clip, L.dtype, s) : muon_launch_momentum(a, L.dtype, s);
+    });
   }
   if (L.kind == kLaunchNorm) {
     NormArgs a;
