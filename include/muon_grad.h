@@ -115,7 +115,8 @@ int muon_grad_clip(const muon_grad_list* list, const muon_clip* clip, void* hip_
 /* muon_grad_norm, then muon_grad_clip by its result. */
 int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm, float* norm, void* hip_stream);
 
-/* AdamW over the list.  hp as adamw_step; clip may be NULL (no clipping). */
+/* AdamW over the list.  hp as adamw_step; clip may be NULL (no clipping), and clip->norm is no
+ * part of a tensor that the list updates. */
 int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream);
 
 /* muon_step whose gradients are scaled by the coefficient of `clip` as the momentum reads

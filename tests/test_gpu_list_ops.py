@@ -210,14 +210,15 @@ HP = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
 
 
 class Adam:
-    """A list of parameters with its state, each buffer guarded; kinds: one per tensor."""
+    """A list of parameters with its state, each buffer guarded; kinds: one per tensor.  apart:
+    the buffers of one tensor lie differently towards the 16 bytes of an access."""
 
-    def __init__(self, sizes, kinds, seed, shift=0, first=False):
+    def __init__(self, sizes, kinds, seed, shift=0, first=False, apart=False):
         self.kinds = [KINDS[k] for k in kinds]
         self.bufs = []
 
-        def part(dtypes, seed, std):
-            views, bufs = make(list(zip(sizes, dtypes)), seed, shift, std)
+        def part(dtypes, at, std):
+            views, bufs = make(list(zip(sizes, dtypes)), at, shift + 3 * (at - seed) if apart else shift, std)
             self.bufs += bufs
             return views
 
@@ -277,6 +278,30 @@ def test_adamw_list(kind, sizes, shift):
     a = Adam(SIZES[sizes], [kind] * len(SIZES[sizes]), 11, shift)
     a.step()(7)
     a.check(7)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_adamw_buffers_that_lie_differently(kind):
+    log(f"adamw {kind}, buffers apart")
+    a = Adam([5, 2048, 4099, 6143, 100_000], [kind] * 5, 17, 1, apart=True)
+    a.step()(2)
+    a.check(2)
+
+
+def test_adamw_offsets_past_32_bits():
+    """More than 2^31 elements, and more chunks than workgroups: every element is updated, once."""
+    n = (1 << 31) + 4099
+    log(f"adamw of {n} elements")
+    p = torch.full((n,), 1.0, device=DEV, dtype=BF16)
+    g = torch.full((n,), 0.5, device=DEV, dtype=BF16)
+    m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    small = [torch.full((5,), x, device=DEV, dtype=t) for x, t in ((1.0, BF16), (0.5, BF16), (0.0, F32), (0.0, F32))]
+    for buf in ((p, g, m, v), small):
+        nm.AdamWStep([buf[0]], [buf[1]], [buf[2]], [buf[3]], lr=0.25, weight_decay=0.0)(1)
+    # The first step moves by lr: 1 - 0.25 m/sqrt(v) = 0.75 after the bf16 rounding.
+    assert float(small[0][0]) == 0.75 and float(small[2][0]) != 0.0
+    for big, one in zip((p, m, v), (small[0], small[2], small[3])):
+        assert int((big == one[0]).sum(dtype=torch.int64)) == n
 
 
 @pytest.mark.parametrize("norm,max_norm", [(4.0, 1.0), (0.5, 1.0), (1.0, 0.0)])
@@ -394,6 +419,42 @@ def test_clip_and_adamw_in_a_graph():
         assert torch.equal(norm, n)
         for x, y in zip(a.g + a.p + a.m + a.v + a.w, b.g + b.p + b.m + b.v + b.w):
             assert torch.equal(x, y)
+
+
+def test_two_graphs_and_eager_calls_share_a_list():
+    """One after another on one stream: each leaves the list as it found it."""
+    log("two graphs, one list")
+    views, _ = make(LISTS["many"] + LISTS["long"], 85, std=1.0)
+    lst = nm.GradClip(views)
+    a, b, e = (torch.zeros((), device=DEV) for _ in range(3))
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        lst.norm(out=a)
+    with torch.cuda.graph(graphs[1]):
+        lst.norm("inf", out=b)
+    for k in range(4):
+        for v in views:
+            v.mul_(0.5 + k)
+        graphs[k % 2].replay()
+        graphs[1 - k % 2].replay()
+        lst.norm(out=e)
+        torch.cuda.synchronize()
+        host = [to64(v) for v in views]
+        assert torch.equal(a, e) and norm_close(a, grad_norm(host)) and float(b) == grad_norm(host, "inf")
+
+
+def test_twenty_thousand_tensors():
+    log("20000 tensors")
+    flat = torch.randn(70_000, device=DEV)
+    sizes = [1 + i % 6 for i in range(20_000)]
+    views = list(flat[:sum(sizes)].split(sizes))
+    host = to64(flat)
+    norm = nm.clip_grad_norm(views, 2.0)
+    assert norm_close(norm, grad_norm([host[:sum(sizes)]]))
+    want = clip_grads([host[:sum(sizes)]], grad_norm([host[:sum(sizes)]]), 2.0)[0]
+    assert np.all(np.abs(to64(flat)[:sum(sizes)] - want) <= clip_bound(want, F32))
+    np.testing.assert_array_equal(to64(flat)[sum(sizes):], host[sum(sizes):])
 
 
 def test_a_list_laid_out_inside_a_graph():
