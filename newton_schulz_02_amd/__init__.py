@@ -838,15 +838,17 @@ class _List:
         """fn(list, *args, stream) on the list's device."""
         import torch
 
-        s = self._stream(stream)
-        if s.cuda_stream != self._home:
+        # The handle alone: a Stream object for the current stream costs as much as the launch.
+        handle = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else \
+            self._stream(stream).cuda_stream
+        if handle != self._home:
             # The allocator keeps the workspace until this stream, too, has passed the call.
-            self.workspace.record_stream(s)
+            self.workspace.record_stream(self._stream(stream))
         if torch.cuda.current_device() == self.device.index:
-            _check(fn(self._list, *args, c_void_p(s.cuda_stream)))
+            _check(fn(self._list, *args, handle))
         else:
             with torch.cuda.device(self.device):
-                _check(fn(self._list, *args, c_void_p(s.cuda_stream)))
+                _check(fn(self._list, *args, handle))
 
 
 class GradClip(_List):
