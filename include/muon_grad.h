@@ -33,9 +33,11 @@
  * Lists: a list is laid out once (muon_grad_list_init, adamw_list_init: the tensors'
  * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used
  * by any number of calls, as long as the tensors stay where they are; their values may
- * change.  The layout is enqueued on the stream given (through kernel arguments: no host buffer, no copy, so it may be
- * captured); uses on another stream must be ordered after it by the caller.  Two calls in
- * flight at once need two lists.  A list is used on the device it was laid out on.
+ * change.  The layout is enqueued on the stream given (through kernel arguments: no host
+ * buffer, no copy, so it may be captured, and the list is then for calls of the same capture
+ * only: its table is not there before a replay); uses on another stream must be ordered after
+ * it by the caller.  Two calls in flight at once need two lists.  A list is used on the device
+ * it was laid out on.
  */
 #ifndef MUON_GRAD_H
 #define MUON_GRAD_H

@@ -774,18 +774,31 @@ def adamw_array(params, grads, ms, vs, masters=None, decays=None):
     if not (n == len(grads) == len(ms) == len(vs) == len(masters) == len(decays)):
         raise ValueError("params, grads, ms, vs, masters and decays must have the same length")
     arr = (adamw_tensor * max(1, n))()
+    codes, f32 = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}, torch.float32
     for i, (p, g, m, v, w, d) in enumerate(zip(params, grads, ms, vs, masters, decays)):
-        for name, t in (("param", p), ("grad", g), ("m", m), ("v", v), ("master", w)):
-            if t is None and name == "master":
-                continue
-            if not t.is_contiguous() or t.shape != p.shape:
-                raise ValueError(f"tensor {i}: {name} must be contiguous and of the param's shape {tuple(p.shape)}")
-            if name in ("m", "v", "master") and t.dtype != torch.float32:
-                raise TypeError(f"tensor {i}: {name} must be float32")
-        arr[i] = adamw_tensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
-                              0 if w is None else w.data_ptr(), p.numel(), _dtype_code(p), _dtype_code(g),
-                              float(d), 0)
+        shape = p.shape
+        pt, gt = codes.get(p.dtype), codes.get(g.dtype)
+        if not (pt and gt and g.shape == shape and m.shape == shape and v.shape == shape and m.dtype == f32 and
+                v.dtype == f32 and p.is_contiguous() and g.is_contiguous() and m.is_contiguous() and
+                v.is_contiguous()) or (w is not None and
+                                       not (w.shape == shape and w.dtype == f32 and w.is_contiguous())):
+            _refuse_adamw(i, p, g, m, v, w)
+        arr[i] = (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), 0 if w is None else w.data_ptr(), p.numel(),
+                  pt, gt, d, 0)
     return arr
+
+
+def _refuse_adamw(i, p, g, m, v, w):
+    import torch
+
+    for name, t in (("param", p), ("grad", g), ("m", m), ("v", v), ("master", w)):
+        if t is None:
+            continue
+        if not t.is_contiguous() or t.shape != p.shape:
+            raise ValueError(f"tensor {i}: {name} must be contiguous and of the param's shape {tuple(p.shape)}")
+        if name in ("m", "v", "master") and t.dtype != torch.float32:
+            raise TypeError(f"tensor {i}: {name} must be float32")
+        _dtype_code(t)
 
 
 def _norm_arg(norm, device):
@@ -821,10 +834,15 @@ class _List:
                 workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
             if workspace.numel() < self.ws_bytes:
                 raise ValueError(f"workspace has {workspace.numel()} bytes, needs {self.ws_bytes}")
+            if workspace.device != self.device:
+                raise ValueError(f"workspace is on {workspace.device}, the list on {self.device}")
             self.workspace = workspace
             self.list = (muon_grad_list if self._kind == "muon_grad_list" else adamw_list)()
             _check(getattr(lib(), f"{self._kind}_init")(arr, count, c_void_p(workspace.data_ptr()), workspace.numel(),
                                                         c_void_p(self._home), ctypes.byref(self.list)))
+            self._captured = torch.cuda.is_current_stream_capturing()
+            self._laid_out = home.record_event()
+        self._ordered = {self._home}  # streams that come after the layout
         self._list = ctypes.byref(self.list)
 
     def _stream(self, stream):
@@ -841,9 +859,10 @@ class _List:
         # The handle alone: a Stream object for the current stream costs as much as the launch.
         handle = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else \
             self._stream(stream).cuda_stream
+        if self._captured and not torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("this list was laid out inside a graph capture and can be used only there")
         if handle != self._home:
-            # The allocator keeps the workspace until this stream, too, has passed the call.
-            self.workspace.record_stream(self._stream(stream))
+            self._elsewhere(self._stream(stream))
         if torch.cuda.current_device() == self.device.index:
             _check(fn(self._list, *args, handle))
         else:
@@ -851,13 +870,29 @@ class _List:
                 _check(fn(self._list, *args, handle))
 
 
+    def _elsewhere(self, stream):
+        """Before a call on another stream than the layout's: it comes after the layout, and the
+        allocator keeps the workspace until it, too, has passed the call."""
+        import torch
+
+        if stream.cuda_stream not in self._ordered:
+            with torch.cuda.stream(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+            # A capture cannot wait for work from outside it; it begins when that work is done.
+            if capturing == self._captured:
+                stream.wait_event(self._laid_out)
+            if not capturing:
+                self._ordered.add(stream.cuda_stream)
+        self.workspace.record_stream(stream)
+
+
 class GradClip(_List):
     """A list of gradients laid out once, for their global norm and clipping by it.
 
     The tensors must stay where they are as long as this is used (their values may change):
     after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
-    `stream` (default: the current one) at construction; a use on another stream must come
-    after it.  Two calls in flight at once need two of these."""
+    `stream` (default: the current one) at construction; calls on other streams wait for it.
+    Two calls in flight at once need two of these."""
 
     _kind = "muon_grad_list"
 
@@ -900,7 +935,8 @@ class AdamWStep(_List):
     """AdamW over fixed lists of device tensors, laid out once (see adamw_array for the lists).
 
     Each call enqueues one ``adamw_list_step`` on the current (or given) stream.  As with
-    GradClip, the tensors stay where they are and the layout goes to `stream`."""
+    GradClip, the tensors stay where they are, the layout goes to `stream`, and two calls in
+    flight at once need two of these."""
 
     _kind = "adamw_list"
 

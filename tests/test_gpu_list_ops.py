@@ -395,6 +395,24 @@ def test_a_list_used_on_another_stream_than_its_own():
     del junk
 
 
+def test_a_call_on_another_stream_waits_for_the_layout():
+    """The layout is queued behind long work on its own stream; the call on a side stream comes
+    after it all the same."""
+    log("layout behind long work")
+    views, _ = make(LISTS["tails"], 71)
+    want = grad_norm([to64(v) for v in views])
+    a = torch.randn(4096, 4096, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        b = a @ a
+    lst = nm.GradClip(views)
+    got = [lst.norm(stream=side), lst.norm(stream=side)]
+    side.synchronize()
+    assert all(norm_close(g, want) for g in got)
+    del b
+
+
 def test_clip_and_adamw_in_a_graph():
     """Captured once and replayed with new values, with eager work in between."""
     log("graph")
@@ -466,6 +484,10 @@ def test_a_list_laid_out_inside_a_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         norm = nm.clip_grad_norm(views, 1.0)
+        inside = nm.GradClip(views)
+        inside.clip(norm, 1e30)
+    with pytest.raises(RuntimeError, match="inside a graph capture"):
+        inside.norm()  # its table exists only in replays
     for k in range(3):
         for v, o in zip(views, other):
             new = torch.randn(v.numel(), device=DEV) * (k + 1)
@@ -495,6 +517,8 @@ def test_refusals_on_the_gpu():
         lst.norm(out=torch.zeros((), device=DEV, dtype=torch.float64))
     with pytest.raises(ValueError, match="workspace"):
         nm.GradClip([g], workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError, match="workspace is on"):
+        nm.GradClip([g], workspace=torch.empty(1 << 20, dtype=torch.uint8))
     p, m, v = torch.ones(10, device=DEV), torch.zeros(10, device=DEV), torch.zeros(10, device=DEV)
     with pytest.raises(nm.MuonError):
         nm.AdamWStep([p], [g], [m], [v])(0)
