@@ -107,7 +107,8 @@ int adamw_list_init(const adamw_tensor* tensors, int32_t count, void* workspace,
                     void* hip_stream, adamw_list* list);
 
 /* *norm <- the norm of all gradients of the list (4-byte aligned device memory that is no part
- * of a gradient).  kind: muon_norm_kind. */
+ * of a gradient; MUON_EALIAS when it lies in the list's workspace, for this and the calls
+ * below).  kind: muon_norm_kind. */
 int muon_grad_norm(const muon_grad_list* list, int32_t kind, float* norm, void* hip_stream);
 
 /* Scale every gradient of the list by the coefficient of `clip`, in place.  Where the
@@ -122,8 +123,8 @@ int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm
 int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream);
 
 /* muon_step whose gradients are scaled by the coefficient of `clip` as the momentum reads
- * them: M <- beta M + c G, in fp32, the gradients
- * unchanged.  clip NULL is muon_step; MUON_EALIAS when clip->norm lies in a param or momentum. */
+ * them: M <- beta M + c G, in fp32, the gradients unchanged.  clip NULL is muon_step;
+ * MUON_EALIAS when clip->norm lies in a param, a momentum or the workspace. */
 int muon_step_clipped(const muon_matrix* mats, int32_t count, const muon_hparams* hp, const muon_clip* clip,
                       void* workspace, size_t workspace_bytes, void* hip_stream);
 

@@ -869,7 +869,6 @@ class _List:
             with torch.cuda.device(self.device):
                 _check(fn(self._list, *args, handle))
 
-
     def _elsewhere(self, stream):
         """Before a call on another stream than the layout's: it comes after the layout, and the
         allocator keeps the workspace until it, too, has passed the call."""

@@ -259,6 +259,17 @@ int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, in
                [&] { return muon_launch_gemm(a, L.dtype, s); });
 }
 
+int check_adamw(const adamw_hparams* hp) {
+  if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+  const float fs[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
+  for (float f : fs)
+    if (!std::isfinite(f)) return fail(MUON_EINVAL, "non-finite hyperparameter");
+  if (hp->step < 1) return fail(MUON_EINVAL, "step must be >= 1");
+  if (hp->beta1 < 0.0f || hp->beta1 >= 1.0f || hp->beta2 < 0.0f || hp->beta2 >= 1.0f)
+    return fail(MUON_EINVAL, "beta1/beta2 outside [0, 1)");
+  return MUON_OK;
+}
+
 int check_max_norm(float max_norm) {
   if (!std::isfinite(max_norm) || max_norm < 0.0f) return fail(MUON_EINVAL, "max_norm is not finite and >= 0");
   return MUON_OK;
@@ -405,19 +416,24 @@ int muon_step(const muon_matrix* mats, int32_t count, const muon_hparams* hp, vo
 
 int muon_step_clipped(const muon_matrix* mats, int32_t count, const muon_hparams* hp, const muon_clip* clip,
                       void* workspace, size_t workspace_bytes, void* hip_stream) {
-  if (!clip) return run_step(mats, count, hp, {nullptr, 0.0f}, workspace, workspace_bytes, hip_stream);
-  const int rc = check_clip(clip);
-  if (rc != MUON_OK) return rc;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(clip->norm);
-  for (int32_t i = 0; mats && i < count; ++i) {
-    const muon_matrix& x = mats[i];
-    if (x.rows < 1 || x.cols < 1 || x.rows >= (int64_t(1) << 31) || x.cols >= (int64_t(1) << 31)) continue;  // refused below
-    const uintptr_t bytes = uintptr_t(x.rows) * uintptr_t(x.cols) * (x.dtype == MUON_BF16 ? 2 : 4);
-    for (const uintptr_t out : {reinterpret_cast<uintptr_t>(x.param), reinterpret_cast<uintptr_t>(x.momentum)})
-      if (at + 4 > out && at < out + bytes)
-        return fail(MUON_EALIAS, "clip: norm lies in an output of matrix " + std::to_string(i));
+  try {
+    if (!clip) return run_step(mats, count, hp, {nullptr, 0.0f}, workspace, workspace_bytes, hip_stream);
+    const int rc = check_clip(clip);
+    if (rc != MUON_OK) return rc;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(clip->norm), ws = reinterpret_cast<uintptr_t>(workspace);
+    if (at + 4 > ws && at - ws < workspace_bytes) return fail(MUON_EALIAS, "clip: norm lies in the workspace");
+    for (int32_t i = 0; mats && i < count; ++i) {
+      const muon_matrix& x = mats[i];
+      if (x.rows < 1 || x.cols < 1 || x.rows >= (int64_t(1) << 31) || x.cols >= (int64_t(1) << 31)) continue;  // refused below
+      const uintptr_t bytes = uintptr_t(x.rows) * uintptr_t(x.cols) * (x.dtype == MUON_BF16 ? 2 : 4);
+      for (const uintptr_t out : {reinterpret_cast<uintptr_t>(x.param), reinterpret_cast<uintptr_t>(x.momentum)})
+        if (at + 4 > out && at < out + bytes)
+          return fail(MUON_EALIAS, "clip: norm lies in an output of matrix " + std::to_string(i));
+    }
+    return run_step(mats, count, hp, {clip->norm, clip->max_norm}, workspace, workspace_bytes, hip_stream);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }
-  return run_step(mats, count, hp, {clip->norm, clip->max_norm}, workspace, workspace_bytes, hip_stream);
 }
 
 namespace {
@@ -883,14 +899,9 @@ int muon_tune_import(const char* text) {
 int adamw_step(float* p, const float* g, float* m, float* v, int64_t n, const adamw_hparams* hp,
                void* hip_stream) {
   try {
-    if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+    const int bad = check_adamw(hp);
+    if (bad != MUON_OK) return bad;
     if (n < 0) return fail(MUON_EINVAL, "n is negative");
-    const float fs[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
-    for (float f : fs)
-      if (!std::isfinite(f)) return fail(MUON_EINVAL, "non-finite hyperparameter");
-    if (hp->step < 1) return fail(MUON_EINVAL, "step must be >= 1");
-    if (hp->beta1 < 0.0f || hp->beta1 >= 1.0f || hp->beta2 < 0.0f || hp->beta2 >= 1.0f)
-      return fail(MUON_EINVAL, "beta1/beta2 outside [0, 1)");
     if (n == 0) return MUON_OK;
     if (!p || !g || !m || !v) return fail(MUON_EINVAL, "NULL pointer");
     const uintptr_t ptrs[4] = {(uintptr_t)p, (uintptr_t)g, (uintptr_t)m, (uintptr_t)v};
@@ -991,6 +1002,14 @@ int on_list_device(const ListHandle& h, int* dev) {
   return check_device(*dev);
 }
 
+// A norm that the list's own workspace holds would be written over.
+int check_norm_place(const ListHandle& h, const float* norm) {
+  const uint64_t at = uint64_t(reinterpret_cast<uintptr_t>(norm));
+  const uint64_t bytes = h.parts_off + (h.magic == kGradListMagic ? kNormParts * sizeof(double) : 0);
+  if (at >= h.workspace && at - h.workspace < bytes) return fail(MUON_EALIAS, "norm lies in the list's workspace");
+  return MUON_OK;
+}
+
 int check_kind(int32_t kind) {
   if (kind != MUON_NORM_L2 && kind != MUON_NORM_INF) return fail(MUON_EINVAL, "unknown kind of norm");
   return MUON_OK;
@@ -1019,17 +1038,6 @@ int launch_clip(int dev, hipStream_t s, const ListHandle& h, const float* norm, 
   GradArgs a = grad_args(h);
   a.clip = {norm, max_norm};
   return timed(dev, s, "grad_clip", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_grad_clip(a, s); });
-}
-
-int check_adamw(const adamw_hparams* hp) {
-  if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
-  const float fs[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
-  for (float f : fs)
-    if (!std::isfinite(f)) return fail(MUON_EINVAL, "non-finite hyperparameter");
-  if (hp->step < 1) return fail(MUON_EINVAL, "step must be >= 1");
-  if (hp->beta1 < 0.0f || hp->beta1 >= 1.0f || hp->beta2 < 0.0f || hp->beta2 >= 1.0f)
-    return fail(MUON_EINVAL, "beta1/beta2 outside [0, 1)");
-  return MUON_OK;
 }
 
 }  // namespace
@@ -1094,6 +1102,7 @@ int muon_grad_norm(const muon_grad_list* list, int32_t kind, float* norm, void* 
     int rc, dev = 0;
     if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
     if ((rc = check_kind(kind)) != MUON_OK || (rc = check_norm(norm)) != MUON_OK) return rc;
+    if ((rc = check_norm_place(h, norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
     if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
@@ -1108,7 +1117,7 @@ int muon_grad_clip(const muon_grad_list* list, const muon_clip* clip, void* hip_
     ListHandle h;
     int rc, dev = 0;
     if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
-    if ((rc = check_clip(clip)) != MUON_OK) return rc;
+    if ((rc = check_clip(clip)) != MUON_OK || (rc = check_norm_place(h, clip->norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
     if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
@@ -1124,6 +1133,7 @@ int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm
     int rc, dev = 0;
     if ((rc = open_list(list, kGradListMagic, &h)) != MUON_OK) return rc;
     if ((rc = check_kind(kind)) != MUON_OK || (rc = check_norm(norm)) != MUON_OK) return rc;
+    if ((rc = check_norm_place(h, norm)) != MUON_OK) return rc;
     if ((rc = check_max_norm(max_norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
@@ -1141,7 +1151,7 @@ int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_
     int rc, dev = 0;
     if ((rc = open_list(list, kAdamListMagic, &h)) != MUON_OK) return rc;
     if ((rc = check_adamw(hp)) != MUON_OK) return rc;
-    if (clip && (rc = check_clip(clip)) != MUON_OK) return rc;
+    if (clip && ((rc = check_clip(clip)) != MUON_OK || (rc = check_norm_place(h, clip->norm)) != MUON_OK)) return rc;
     AdamListArgs a;
     std::memset(&a, 0, sizeof a);
     const char* ws = reinterpret_cast<const char*>(uintptr_t(h.workspace));

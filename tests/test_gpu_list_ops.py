@@ -519,6 +519,11 @@ def test_refusals_on_the_gpu():
         nm.GradClip([g], workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="workspace is on"):
         nm.GradClip([g], workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    inside = lst.workspace[4096:4100].view(F32)
+    for call in (lambda: lst.norm(out=inside), lambda: lst.clip(inside, 1.0), lambda: lst.clip_norm(1.0, out=inside)):
+        with pytest.raises(nm.MuonError) as e:
+            call()
+        assert e.value.status == nm.MUON_EALIAS
     p, m, v = torch.ones(10, device=DEV), torch.zeros(10, device=DEV), torch.zeros(10, device=DEV)
     with pytest.raises(nm.MuonError):
         nm.AdamWStep([p], [g], [m], [v])(0)

@@ -167,7 +167,7 @@ def test_clipped_muon_step_refusals():
     def run(norm=1 << 30, max_norm=1.0, reserved=0, arr=None):
         clip = nm.muon_clip(norm, max_norm, reserved)
         return nm.lib().muon_step_clipped(arr or mats((8, 8), (8, 16)), 2, ctypes.byref(HP), ctypes.byref(clip),
-                                          ctypes.c_void_p(1 << 32), 1 << 40, None)
+                                          ctypes.c_void_p(1 << 32), 1 << 39, None)
 
     a = mats((8, 8), (8, 16))
     assert run(norm=0) == nm.MUON_EINVAL and run(norm=(1 << 30) + 2) == nm.MUON_EINVAL
@@ -175,6 +175,8 @@ def test_clipped_muon_step_refusals():
     assert run(max_norm=math.nan) == nm.MUON_EINVAL and run(reserved=1) == nm.MUON_EINVAL
     for out, n in ((a[0].param, 8 * 8 * 2), (a[1].momentum, 8 * 16 * 2)):
         assert run(norm=out) == nm.MUON_EALIAS and run(norm=out + n - 4) == nm.MUON_EALIAS
+    for at in (1 << 32, (1 << 32) + (1 << 39) - 4):
+        assert run(norm=at) == nm.MUON_EALIAS  # in the workspace
     if not _gpu_visible():  # just outside: valid, and stops at the first HIP call
         assert run(norm=a[0].param - 4) == nm.MUON_EHIP and run(norm=a[0].param + 8 * 8 * 2) == nm.MUON_EHIP
     bad = mats((8, 8), (8, 16))
