@@ -9,7 +9,7 @@
 //          sums hide under the loads: the inf norm, an integer maximum, is 1 % faster.
 //   clip   reads and writes them: 126 us, 6.4 TB/s; 450 us, 6.3 TB/s.
 //   AdamW  reads and writes its state once: two 32000 x 4096 embeddings with masters and bf16
-//          gradients (7.3 GB) in 1.23 ms, 6.0 TB/s.
+//          gradients (7.3 GB) in 1.17 ms, 6.3 TB/s.
 // (A copy by the runtime's own kernel moves 4.9 TB/s on the same card.)
 #include <hip/hip_runtime.h>
 
@@ -305,7 +305,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&f)[4]) {
 // one flat bucket per type) are all read and written by whole lines.
 // All loads of a whole chunk are in flight before the first update: 16 bytes of fp32 per lane
 // and load, two of each buffer.  Non-temporal loads and stores together are worth a tenth
-// (embeddings with masters 1.36 -> 1.23 ms), either alone nothing.  Dividing by reciprocals
+// (embeddings with masters 1.36 -> 1.21 ms), either alone nothing.  Dividing by reciprocals
 // instead changes nothing: the arithmetic hides under the loads.
 template <typename P, typename G, bool MASTER>
 __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float coef, const AdamListArgs& a) {
@@ -382,9 +382,20 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
   }
 }
 
+// Workgroups go to the eight XCDs in turn: each round of 128 chunks gives every XCD 16
+// neighbouring ones, longer runs of each of the nine streams.  us with 1 / 8 / 16 / 32:
+// embeddings with masters 1211 / 1227 / 1161 / 1162, fp32 303 / 303 / 296 / 307, bf16 467 / 466 /
+// 456 / 456; the norm and clipping, of one stream or two, gain nothing.
+__device__ __forceinline__ uint32_t chunk_of(uint32_t b, uint32_t chunks) {
+  constexpr uint32_t kRun = 16, kRound = 8 * kRun;
+  const uint32_t base = b / kRound * kRound, i = b - base;
+  return base + kRound > chunks ? b : base + i % 8 * kRun + i / 8;
+}
+
 __global__ __launch_bounds__(256) void k_adamw_list(AdamListArgs a) {
   const float coef = clip_coef(a.clip);
-  for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+  for (uint32_t b = blockIdx.x; b < a.chunks; b += gridDim.x) {
+    const uint32_t c = chunk_of(b, a.chunks);
     const AdamRec& r = a.recs[a.map[c]];
     if (!r.param_bf16) {
       if (r.grad_bf16) adamw_chunk<float, uint16_t, false>(r, c, coef, a);
