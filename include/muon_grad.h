@@ -34,9 +34,9 @@
  * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used
  * by any number of calls, as long as the tensors stay where they are; their values may
  * change.  The layout is enqueued on the stream given (through kernel arguments: no host
- * buffer, no copy, so it may be captured, and the list is then for calls of the same capture
- * only: its table is not there before a replay); uses on another stream must be ordered after
- * it by the caller.  Two calls in flight at once need two lists.  A list is used on the device
+ * buffer, no copy, so it may be captured, and the list is then for calls on streams of the same
+ * capture only, MUON_EINVAL elsewhere: its table is not there before a replay); uses on another
+ * stream must be ordered after it by the caller.  Two calls in flight at once need two lists.  A list is used on the device
  * it was laid out on.
  */
 #ifndef MUON_GRAD_H
@@ -105,6 +105,11 @@ int muon_grad_list_init(const muon_grad* grads, int32_t count, void* workspace, 
                         void* hip_stream, muon_grad_list* list);
 int adamw_list_init(const adamw_tensor* tensors, int32_t count, void* workspace, size_t workspace_bytes,
                     void* hip_stream, adamw_list* list);
+
+/* *capture <- the identity of the graph capture that hip_stream takes part in, 0 for none:
+ * what tells whether a list that was laid out in a capture can be used on the stream.
+ * Enqueues nothing.  MUON_EINVAL for a capture that was broken off. */
+int muon_stream_capture(void* hip_stream, uint64_t* capture);
 
 /* *norm <- the norm of all gradients of the list (4-byte aligned device memory that is no part
  * of a gradient; MUON_EALIAS when it lies in the list's workspace, for this and the calls

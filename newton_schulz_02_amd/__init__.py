@@ -141,6 +141,7 @@ _SIGNATURES = {
     "muon_step_clipped": (c_int, [_MATP, c_int32, _HPP, POINTER(muon_clip), c_void_p, c_size_t, c_void_p]),
     "muon_grad_list_size": (c_int, [POINTER(muon_grad), c_int32, POINTER(c_size_t)]),
     "muon_grad_list_init": (c_int, [POINTER(muon_grad), c_int32, c_void_p, c_size_t, c_void_p, POINTER(muon_grad_list)]),
+    "muon_stream_capture": (c_int, [c_void_p, POINTER(c_uint64)]),
     "muon_grad_norm": (c_int, [POINTER(muon_grad_list), c_int32, c_void_p, c_void_p]),
     "muon_grad_clip": (c_int, [POINTER(muon_grad_list), POINTER(muon_clip), c_void_p]),
     "muon_grad_clip_norm": (c_int, [POINTER(muon_grad_list), c_int32, c_float, c_void_p, c_void_p]),
@@ -814,6 +815,13 @@ def _clip_arg(clip, device):
     return ctypes.byref(muon_clip(_norm_arg(norm, device), float(max_norm), 0))
 
 
+def _capture_of(handle: int) -> int:
+    """The identity of the graph capture that a stream takes part in, 0 for none."""
+    out = c_uint64(0)
+    _check(lib().muon_stream_capture(c_void_p(handle), ctypes.byref(out)))
+    return out.value
+
+
 class _List:
     """A list of tensors laid out on one device: what GradClip and AdamWStep share."""
 
@@ -840,7 +848,7 @@ class _List:
             self.list = (muon_grad_list if self._kind == "muon_grad_list" else adamw_list)()
             _check(getattr(lib(), f"{self._kind}_init")(arr, count, c_void_p(workspace.data_ptr()), workspace.numel(),
                                                         c_void_p(self._home), ctypes.byref(self.list)))
-            self._captured = torch.cuda.is_current_stream_capturing()
+            self._capture = _capture_of(self._home)
             self._laid_out = home.record_event()
         self._ordered = {self._home}  # streams that come after the layout
         self._list = ctypes.byref(self.list)
@@ -852,15 +860,23 @@ class _List:
             return torch.cuda.current_stream(self.device)
         return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
 
-    def _call(self, fn, args, stream):
-        """fn(list, *args, stream) on the list's device."""
+    def _handle(self, stream):
+        """The handle of the stream of a call, which may use the list."""
         import torch
 
         # The handle alone: a Stream object for the current stream costs as much as the launch.
         handle = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else \
             self._stream(stream).cuda_stream
-        if self._captured and not torch.cuda.is_current_stream_capturing():
+        # Before the call allocates, or waits for anything: a wait for the layout would pull its
+        # stream into the layout's capture, or break its own.
+        if self._capture and _capture_of(handle) != self._capture:
             raise RuntimeError("this list was laid out inside a graph capture and can be used only there")
+        return handle
+
+    def _call(self, fn, args, stream, handle):
+        """fn(list, *args, stream) on the list's device."""
+        import torch
+
         if handle != self._home:
             self._elsewhere(self._stream(stream))
         if torch.cuda.current_device() == self.device.index:
@@ -872,15 +888,12 @@ class _List:
     def _elsewhere(self, stream):
         """Before a call on another stream than the layout's: it comes after the layout, and the
         allocator keeps the workspace until it, too, has passed the call."""
-        import torch
-
         if stream.cuda_stream not in self._ordered:
-            with torch.cuda.stream(stream):
-                capturing = torch.cuda.is_current_stream_capturing()
+            capture = _capture_of(stream.cuda_stream)
             # A capture cannot wait for work from outside it; it begins when that work is done.
-            if capturing == self._captured:
+            if capture == self._capture:
                 stream.wait_event(self._laid_out)
-            if not capturing:
+            if not capture:
                 self._ordered.add(stream.cuda_stream)
         self.workspace.record_stream(stream)
 
@@ -891,6 +904,7 @@ class GradClip(_List):
     The tensors must stay where they are as long as this is used (their values may change):
     after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
     `stream` (default: the current one) at construction; calls on other streams wait for it.
+    Inside a graph capture it is recorded, and only calls on streams of that capture can use it.
     Two calls in flight at once need two of these."""
 
     _kind = "muon_grad_list"
@@ -912,21 +926,22 @@ class GradClip(_List):
     def norm(self, kind="l2", *, out=None, stream=None):
         """The norm of all gradients, as a float32 device tensor (`out`, or a new one that
         belongs to the stream of the call)."""
-        code = _norm_kind(kind)
+        code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream)
+        self._call(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
         return out
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
         """Scale the gradients in place by min(1, max_norm / (norm + 1e-6)); `norm` is a float32
         device tensor, for example one that was reduced over ranks."""
-        self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream)
+        handle = self._handle(stream)
+        self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream, handle)
 
     def clip_norm(self, max_norm, kind="l2", *, out=None, stream=None):
         """norm(), then clip() by it; returns the norm from before."""
-        code = _norm_kind(kind)
+        code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream)
+        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream, handle)
         return out
 
 
@@ -951,11 +966,12 @@ class AdamWStep(_List):
     def __call__(self, step, *, lr=None, clip=None, stream=None) -> None:
         """Update number `step` (>= 1), with `lr` from now on if given; clip = (norm, max_norm)
         scales the gradients by min(1, max_norm / (norm + 1e-6)) as they are read."""
+        handle = self._handle(stream)
         self.hp.step = int(step)
         if lr is not None:
             self.hp.lr = float(lr)
         arg = None if clip is None else _clip_arg(clip, self.device)
-        self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream)
+        self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream, handle)
 
 
 def grad_norm(grads, kind="l2", *, device=None, stream=None):

@@ -48,8 +48,7 @@ void lay_out(const std::vector<Rec>& recs, ListTable* t) {
   t->words.assign((kListHead + recs.size() * sizeof(Rec)) / 4, 0);
   if (!recs.empty()) std::memcpy(t->words.data() + kListHead / 4, recs.data(), recs.size() * sizeof(Rec));
   t->map_off = size_t(round_up(int64_t(t->words.size()) * 4, 256));
-  t->parts_off = t->map_off + size_t(round_up(int64_t(t->chunks) * 4, 256));
-  t->ws_bytes = t->parts_off;
+  t->ws_bytes = end_of_map(t->map_off, t->chunks);
 }
 
 int check_count(const void* list, int32_t count, std::string* err) {

@@ -35,7 +35,7 @@ struct ListTable {
   int64_t elems = 0;
   double read_bytes = 0.0;      // gradients (all operands of an AdamW list) read once
   double write_bytes = 0.0;     // outputs written once
-  size_t map_off = 0, parts_off = 0;  // bytes from the workspace's start
+  size_t map_off = 0;           // bytes from the workspace's start; the norm's partial results follow the map
   size_t ws_bytes = 0;
 };
 
@@ -52,7 +52,8 @@ struct ListHandle {
   uint64_t workspace;
   uint32_t chunks;
   int32_t device;
-  uint64_t map_off, parts_off;
+  uint64_t map_off;
+  uint64_t capture;   // the graph capture the layout was recorded in, 0: none
   double read_bytes, write_bytes;
   uint64_t check;     // over the fields above: an uninitialised or foreign handle is refused
 };
@@ -60,5 +61,10 @@ constexpr uint64_t kGradListMagic = 0x6d756f6e67726164ull;
 constexpr uint64_t kAdamListMagic = 0x6d756f6e6164616dull;
 
 uint64_t handle_check(const ListHandle& h);
+
+// Bytes from the workspace's start to what follows the map of a list's chunks.
+inline size_t end_of_map(size_t map_off, uint32_t chunks) {
+  return map_off + size_t(round_up(int64_t(chunks) * 4, 256));
+}
 
 }  // namespace muon

@@ -943,6 +943,18 @@ namespace {
 static_assert(sizeof(ListHandle) == sizeof(muon_grad_list) && sizeof(ListHandle) == sizeof(adamw_list),
               "a laid-out list holds one handle");
 
+// The identity of the capture that a stream takes part in, 0 for none.  A capture that was
+// broken off is refused.
+int capture_of(hipStream_t s, uint64_t* id) {
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  unsigned long long x = 0;
+  const hipError_t e = hipStreamGetCaptureInfo(s, &status, &x);
+  if (e != hipSuccess) return hip_fail(e, "hipStreamGetCaptureInfo");
+  if (status == hipStreamCaptureStatusInvalidated) return fail(MUON_EINVAL, "the stream's graph capture was broken off");
+  *id = status == hipStreamCaptureStatusActive ? uint64_t(x) : 0;
+  return MUON_OK;
+}
+
 // Write a list's table to its workspace and fill its handle.
 int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t workspace_bytes, void* hip_stream,
               void* list) {
@@ -962,6 +974,7 @@ int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t worksp
   int rc = MUON_OK, dev = 0;
   if ((rc = current_device(&dev)) != MUON_OK) return rc;
   if ((rc = check_device(dev)) != MUON_OK) return rc;
+  if ((rc = capture_of(static_cast<hipStream_t>(hip_stream), &h.capture)) != MUON_OK) return rc;
   const int e = muon_put_words(workspace, t.words.data(), t.words.size() * 4, hip_stream);
   if (e != hipSuccess) return hip_fail(hipError_t(e), "list layout (kernel arguments)");
   char* ws = static_cast<char*>(workspace);
@@ -975,7 +988,6 @@ int init_list(const ListTable& t, uint64_t magic, void* workspace, size_t worksp
   h.chunks = t.chunks;
   h.device = dev;
   h.map_off = t.map_off;
-  h.parts_off = t.parts_off;
   h.read_bytes = t.read_bytes;
   h.write_bytes = t.write_bytes;
   h.check = handle_check(h);
@@ -992,20 +1004,29 @@ int open_list(const void* list, uint64_t magic, ListHandle* h) {
   return MUON_OK;
 }
 
-// Caller holds g_mu.
-int on_list_device(const ListHandle& h, int* dev) {
+// The call's device and stream are ones that the list can be used on.  Caller holds g_mu.
+int check_list_place(const ListHandle& h, hipStream_t s, int* dev) {
   int rc;
   if ((rc = current_device(dev)) != MUON_OK) return rc;
   if (*dev != h.device)
     return fail(MUON_EINVAL, "the list was laid out on device " + std::to_string(h.device) + ", the current one is " +
                                  std::to_string(*dev));
-  return check_device(*dev);
+  if ((rc = check_device(*dev)) != MUON_OK) return rc;
+  if (h.capture) {
+    // Its table is written by replays of that capture's graph, and by nothing else: a call
+    // anywhere else could follow whatever lies in the workspace.
+    uint64_t id = 0;
+    if ((rc = capture_of(s, &id)) != MUON_OK) return rc;
+    if (id != h.capture)
+      return fail(MUON_EINVAL, "the list was laid out inside a graph capture and can be used only on streams of that capture");
+  }
+  return MUON_OK;
 }
 
 // A norm that the list's own workspace holds would be written over.
 int check_norm_place(const ListHandle& h, const float* norm) {
   const uint64_t at = uint64_t(reinterpret_cast<uintptr_t>(norm));
-  const uint64_t bytes = h.parts_off + (h.magic == kGradListMagic ? kNormParts * sizeof(double) : 0);
+  const uint64_t bytes = end_of_map(h.map_off, h.chunks) + (h.magic == kGradListMagic ? kNormParts * sizeof(double) : 0);
   if (at >= h.workspace && at - h.workspace < bytes) return fail(MUON_EALIAS, "norm lies in the list's workspace");
   return MUON_OK;
 }
@@ -1023,7 +1044,7 @@ GradArgs grad_args(const ListHandle& h) {
   a.map = reinterpret_cast<const uint32_t*>(ws + h.map_off);
   a.chunks = h.chunks;
   a.tickets = reinterpret_cast<uint32_t*>(ws + kListTickets);
-  a.parts = reinterpret_cast<double*>(ws + h.parts_off);
+  a.parts = reinterpret_cast<double*>(ws + end_of_map(h.map_off, h.chunks));
   return a;
 }
 
@@ -1041,6 +1062,15 @@ int launch_clip(int dev, hipStream_t s, const ListHandle& h, const float* norm, 
 }
 
 }  // namespace
+
+int muon_stream_capture(void* hip_stream, uint64_t* capture) {
+  try {
+    if (!capture) return fail(MUON_EINVAL, "capture is NULL");
+    return capture_of(static_cast<hipStream_t>(hip_stream), capture);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
 
 int muon_grad_list_size(const muon_grad* grads, int32_t count, size_t* bytes) {
   try {
@@ -1105,7 +1135,7 @@ int muon_grad_norm(const muon_grad_list* list, int32_t kind, float* norm, void* 
     if ((rc = check_norm_place(h, norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
     return launch_norm(dev, s, h, kind, norm);
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
@@ -1120,7 +1150,7 @@ int muon_grad_clip(const muon_grad_list* list, const muon_clip* clip, void* hip_
     if ((rc = check_clip(clip)) != MUON_OK || (rc = check_norm_place(h, clip->norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
     return launch_clip(dev, s, h, clip->norm, clip->max_norm);
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
@@ -1137,7 +1167,7 @@ int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm
     if ((rc = check_max_norm(max_norm)) != MUON_OK) return rc;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
     if ((rc = launch_norm(dev, s, h, kind, norm)) != MUON_OK) return rc;
     return launch_clip(dev, s, h, norm, max_norm);
   } catch (const std::exception& e) {
@@ -1168,7 +1198,7 @@ int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_
     a.bc2 = float(1.0 - std::pow(double(hp->beta2), double(hp->step)));
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = on_list_device(h, &dev)) != MUON_OK) return rc;
+    if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
     return timed(dev, s, "adamw_list", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_adamw_list(a, s); });
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());

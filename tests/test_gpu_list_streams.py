@@ -1,0 +1,79 @@
+"""GPU: the list operators in graph captures and on streams of their own.  Tolerances as in
+test_gpu_list_ops."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import newton_schulz_02_amd as nm
+from oracle.grad_oracle import grad_norm
+from tests.gpu_helpers import DEV, log, to64
+from tests.test_gpu_list_ops import LISTS, make, norm_close
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_list_of_one_capture_is_refused_in_another():
+    """The second capture would record calls on a table that only replays of the first write.
+    Nothing of the refused calls is recorded."""
+    log("list of another capture")
+    views, _ = make(LISTS["tails"], 100, std=1.0)
+    p, m, v = ([torch.zeros_like(x, dtype=torch.float32) for x in views] for _ in range(3))
+    norm, other = torch.zeros((), device=DEV), torch.ones((), device=DEV)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.graph(graphs[0]):
+        lst = nm.GradClip(views)
+        adam = nm.AdamWStep(p, views, m, v)
+        lst.norm(out=norm)
+    with torch.cuda.graph(graphs[1]):
+        other.add_(1.0)
+        calls = [lambda: lst.norm(out=other), lambda: lst.norm(), lambda: lst.clip(norm, 1.0),
+                 lambda: lst.clip_norm(1.0, out=other), lambda: adam(1)]
+        for call in calls:
+            with pytest.raises(RuntimeError, match="inside a graph capture"):
+                call()
+        # The library's own check, for callers without the binding.
+        stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        assert nm.lib().muon_grad_norm(ctypes.byref(lst.list), 0, ctypes.c_void_p(other.data_ptr()),
+                                       stream) == nm.MUON_EINVAL
+        assert "inside a graph capture" in nm.last_error()
+        hp = nm.adamw_hparams(1e-3, 0.9, 0.95, 1e-8, 0.1, 1)
+        assert nm.lib().adamw_list_step(ctypes.byref(adam.list), ctypes.byref(hp), None, stream) == nm.MUON_EINVAL
+    for k in range(3):
+        graphs[1].replay()  # before the first one: only the addition
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert float(other) == 2.0 + k
+        assert norm_close(norm, grad_norm([to64(x) for x in views]))
+        for x in views:
+            x.mul_(0.5)
+    assert not any(bool(t.any()) for t in p + m + v)
+
+
+def test_a_captured_list_on_streams_beside_its_capture():
+    """Refused on a stream that has not joined the capture; used on one that has."""
+    log("list and a side stream of a capture")
+    views, _ = make(LISTS["tails"], 101, std=1.0)
+    norm, apart = torch.zeros((), device=DEV), torch.zeros((), device=DEV)
+    side, stranger = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)  # joins before the layout, which the call waits for all the same
+        lst = nm.GradClip(views)
+        for out in (apart, None):
+            with pytest.raises(RuntimeError, match="inside a graph capture"):
+                lst.norm(out=out, stream=stranger)
+        lst.norm(out=norm, stream=side)
+        main.wait_stream(side)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert norm_close(norm, grad_norm([to64(x) for x in views])) and float(apart) == 0.0
+        for x in views:
+            x.mul_(0.5)

@@ -1,0 +1,102 @@
+"""CPU tests of how the list classes deal with streams and graph captures, with the stream calls
+replaced by recorders: no test here launches a kernel."""
+
+from __future__ import annotations
+
+import ctypes
+import types
+
+import pytest
+import torch
+
+import newton_schulz_02_amd as nm
+from tests.test_abi import _gpu_visible
+
+
+class Stream:
+    """Stands in for a stream: its handle, the capture it takes part in, and what was asked of it."""
+
+    def __init__(self, handle, capture=0):
+        self.cuda_stream, self.capture, self.waits, self.device = handle, capture, [], torch.device("cuda", 0)
+
+    def wait_event(self, event):
+        self.waits.append(event)
+
+    def record_event(self):
+        return ("event of", self.cuda_stream, self.capture)
+
+
+def laid_out(home, cls=nm.GradClip):
+    """A list laid out on `home`, without a device."""
+    lst = object.__new__(cls)
+    lst.device, lst.count = torch.device("cuda", 0), 0
+    lst._home, lst._capture, lst._laid_out = home.cuda_stream, home.capture, home.record_event()
+    lst._ordered = {lst._home}
+    lst.workspace = types.SimpleNamespace(record_stream=lambda s: None)
+    lst.list = lst._list = None
+    return lst
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Streams by handle; the library's and torch's answers on them."""
+    known = {}
+
+    def make(handle, capture=0):
+        known[handle] = Stream(handle, capture)
+        return known[handle]
+
+    monkeypatch.setattr(nm, "_capture_of", lambda handle: known[handle].capture)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return make
+
+
+def calls():
+    seen = []
+
+    def fn(*args):
+        seen.append(args)
+        return nm.MUON_OK
+    return fn, seen
+
+
+def use(lst, stream):
+    fn, seen = calls()
+    lst._call(fn, (), stream, lst._handle(stream))
+    return seen
+
+
+def test_a_captured_list_is_for_streams_of_its_capture(streams):
+    home = streams(1, capture=7)
+    lst = laid_out(home)
+    assert use(lst, home) and not home.waits
+    # A branch of the same capture waits for the layout, each time.
+    branch = streams(2, capture=7)
+    assert use(lst, branch) and use(lst, branch)
+    assert branch.waits == [lst._laid_out] * 2
+    # Nothing is asked of a stream outside, and no call is made.
+    for other in (streams(3), streams(4, capture=8)):
+        with pytest.raises(RuntimeError, match="inside a graph capture"):
+            use(lst, other)
+        assert not other.waits
+    # The same stream in a later capture, and after both.
+    for capture in (8, 0):
+        home.capture = capture
+        with pytest.raises(RuntimeError, match="inside a graph capture"):
+            use(lst, home)
+
+
+def test_an_eager_list_waits_once_for_its_layout(streams):
+    lst = laid_out(streams(1))
+    side = streams(2)
+    assert use(lst, side) and use(lst, side)
+    assert side.waits == [lst._laid_out]
+    graph = streams(3, capture=7)  # cannot wait for what is outside
+    assert use(lst, graph) and not graph.waits
+
+
+def test_stream_capture_arguments():
+    out = ctypes.c_uint64(5)
+    assert nm.lib().muon_stream_capture(None, None) == nm.MUON_EINVAL
+    if not _gpu_visible():
+        assert nm.lib().muon_stream_capture(None, ctypes.byref(out)) == nm.MUON_EHIP and out.value == 5
