@@ -905,12 +905,15 @@ class GradClip(_List):
     after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
     `stream` (default: the current one) at construction; calls on other streams wait for it.
     Inside a graph capture it is recorded, and only calls on streams of that capture can use it.
-    Two calls in flight at once need two of these."""
+    Norms on several streams run in the order of the calls.  Replays of graphs are not calls:
+    graphs that hold norms of one list are replayed one after another (and after eager norms of
+    it), or each has a list of its own."""
 
     _kind = "muon_grad_list"
 
     def __init__(self, grads, *, device=None, workspace=None, stream=None):
         self.grads = list(grads)
+        self._norm_last, self._norm_streams = None, {}
         self._lay_out(grad_array(self.grads), len(self.grads), self.grads, device, workspace, stream)
 
     def _out(self, out, stream):
@@ -923,12 +926,33 @@ class GradClip(_List):
         with torch.cuda.stream(self._stream(stream)):
             return torch.empty((), dtype=torch.float32, device=self.device)
 
+    def _call_norm(self, fn, args, stream, handle):
+        if handle != self._norm_last:
+            self._in_turn(self._stream(stream))
+        self._call(fn, args, stream, handle)
+
+    def _in_turn(self, stream):
+        """Before a norm on another stream than the last one's: norms of a list count their
+        workgroups in the list's workspace, so each comes after those before it.  A capture waits
+        only for the norms inside it, and nothing outside waits for those."""
+        capture, still = _capture_of(stream.cuda_stream), {}
+        for handle, other in self._norm_streams.items():
+            if handle == stream.cuda_stream:
+                continue
+            inside = _capture_of(handle)
+            if inside == capture:
+                stream.wait_event(other.record_event())
+            if inside or capture:
+                still[handle] = other
+        still[stream.cuda_stream] = stream
+        self._norm_last, self._norm_streams = stream.cuda_stream, still
+
     def norm(self, kind="l2", *, out=None, stream=None):
         """The norm of all gradients, as a float32 device tensor (`out`, or a new one that
         belongs to the stream of the call)."""
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
+        self._call_norm(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
         return out
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
@@ -941,7 +965,8 @@ class GradClip(_List):
         """norm(), then clip() by it; returns the norm from before."""
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream, handle)
+        self._call_norm(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream,
+                        handle)
         return out
 
 
@@ -949,8 +974,8 @@ class AdamWStep(_List):
     """AdamW over fixed lists of device tensors, laid out once (see adamw_array for the lists).
 
     Each call enqueues one ``adamw_list_step`` on the current (or given) stream.  As with
-    GradClip, the tensors stay where they are, the layout goes to `stream`, and two calls in
-    flight at once need two of these."""
+    GradClip, the tensors stay where they are and the layout goes to `stream`.  Every call updates
+    the tensors, so the caller orders calls on several streams."""
 
     _kind = "adamw_list"
 

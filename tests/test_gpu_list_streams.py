@@ -77,3 +77,46 @@ def test_a_captured_list_on_streams_beside_its_capture():
         assert norm_close(norm, grad_norm([to64(x) for x in views])) and float(apart) == 0.0
         for x in views:
             x.mul_(0.5)
+
+
+def test_norms_of_one_list_on_streams_in_turn():
+    """Called on three streams with no waits of the caller's own: each norm comes after the last
+    one, whose counts and partial results lie in the same workspace."""
+    log("norms in turn")
+    views, _ = make(LISTS["long"] + LISTS["many"], 102, std=1.0)
+    host = [to64(x) for x in views]
+    want = {kind: grad_norm(host, kind) for kind in ("l2", "inf")}
+    lst = nm.GradClip(views)
+    torch.cuda.synchronize()
+    streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for k in range(30):
+        kind = ("l2", "inf")[k % 2]
+        outs.append((kind, lst.norm(kind, stream=streams[k * 7 % 3])))
+    torch.cuda.synchronize()
+    for kind, got in outs:
+        assert norm_close(got, want[kind])
+
+
+def test_norms_of_one_list_on_branches_of_a_capture():
+    log("norms on branches")
+    views, _ = make(LISTS["long"], 103, std=1.0)
+    lst = nm.GradClip(views)
+    outs = [torch.zeros((), device=DEV) for _ in range(4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for k, out in enumerate(outs):
+            lst.norm(out=out, stream=side if k % 2 else None)
+        main.wait_stream(side)
+    for k in range(4):
+        graph.replay()
+        eager = lst.norm()
+        torch.cuda.synchronize()
+        want = grad_norm([to64(x) for x in views])
+        assert all(torch.equal(out, eager) for out in outs) and norm_close(eager, want)
+        for x in views:
+            x.mul_(0.5)

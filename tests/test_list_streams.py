@@ -32,6 +32,7 @@ def laid_out(home, cls=nm.GradClip):
     lst.device, lst.count = torch.device("cuda", 0), 0
     lst._home, lst._capture, lst._laid_out = home.cuda_stream, home.capture, home.record_event()
     lst._ordered = {lst._home}
+    lst._norm_last, lst._norm_streams = None, {}
     lst.workspace = types.SimpleNamespace(record_stream=lambda s: None)
     lst.list = lst._list = None
     return lst
@@ -93,6 +94,69 @@ def test_an_eager_list_waits_once_for_its_layout(streams):
     assert side.waits == [lst._laid_out]
     graph = streams(3, capture=7)  # cannot wait for what is outside
     assert use(lst, graph) and not graph.waits
+
+
+def norm(lst, stream):
+    fn, seen = calls()
+    lst._call_norm(fn, (), stream, lst._handle(stream))
+    assert len(seen) == 1
+
+
+def waited(stream, lst):
+    """Streams that `stream` was made to wait for (the layout aside), and forget them."""
+    out = [e[1] for e in stream.waits if e is not lst._laid_out]
+    stream.waits.clear()
+    return out
+
+
+def test_norms_of_a_list_come_one_after_another(streams):
+    a, b, c = (streams(k) for k in (1, 2, 3))
+    lst = laid_out(a)
+    norm(lst, a)
+    norm(lst, a)
+    assert not a.waits
+    norm(lst, b)
+    assert waited(b, lst) == [1]
+    norm(lst, b)
+    assert not b.waits
+    norm(lst, c)
+    assert waited(c, lst) == [2]
+    norm(lst, a)
+    assert waited(a, lst) == [3]
+
+
+def test_norms_inside_a_capture_and_outside_do_not_wait_for_each_other(streams):
+    a, b, c, d = (streams(k) for k in (1, 2, 3, 4))
+    lst = laid_out(a)
+    norm(lst, a)
+    b.capture = c.capture = 7
+    norm(lst, b)
+    assert waited(b, lst) == []
+    norm(lst, c)  # a branch of the same capture
+    assert waited(c, lst) == [2]
+    norm(lst, d)  # eager: the eager norm before it was on a
+    assert waited(d, lst) == [1]
+    norm(lst, c)
+    assert waited(c, lst) == [2]  # b's capture goes on
+    d.capture = 9  # d's eager norm was before this capture, so nothing can wait for it
+    norm(lst, a)
+    assert waited(a, lst) == []
+    b.capture = c.capture = d.capture = 0
+    norm(lst, b)
+    assert set(waited(b, lst)) == {1, 3, 4}
+    norm(lst, a)
+    assert waited(a, lst) == [2]
+
+
+def test_a_branch_waits_for_a_norm_that_its_origin_captured(streams):
+    """The origin stream held the last norm before the capture, too."""
+    a, b = streams(1), streams(2)
+    lst = laid_out(a)
+    norm(lst, a)
+    a.capture = b.capture = 7
+    norm(lst, a)
+    norm(lst, b)
+    assert waited(b, lst) == [1]
 
 
 def test_stream_capture_arguments():
