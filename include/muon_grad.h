@@ -36,8 +36,10 @@
  * change.  The layout is enqueued on the stream given (through kernel arguments: no host
  * buffer, no copy, so it may be captured, and the list is then for calls on streams of the same
  * capture only, MUON_EINVAL elsewhere: its table is not there before a replay); uses on another
- * stream must be ordered after it by the caller.  Two calls in flight at once need two lists.  A list is used on the device
- * it was laid out on.
+ * stream must be ordered after it by the caller.  Calls of a list, replays of graphs that hold
+ * them among these, come one after another (two at once need two lists): two norms at once mix
+ * their partial results, and what they write is undefined.  Later calls are right again.  A list
+ * is used on the device it was laid out on.
  */
 #ifndef MUON_GRAD_H
 #define MUON_GRAD_H

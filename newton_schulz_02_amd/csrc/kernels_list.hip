@@ -206,9 +206,11 @@ __device__ __forceinline__ double reduce(double x, bool inf, double* red) {
 // back a whole L2, and one per workgroup took 36 us over 1024 workgroups.  Counts of one
 // address are made one after another (10 ns each), so a workgroup counts itself among those
 // with its index modulo kTickets, and the last of each of these among the last ones; up to 64
-// workgroups count themselves at once.  All counts are back at 0 at the end.
-__device__ __forceinline__ uint32_t count_self(uint32_t* ticket) {
-  return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// workgroups count themselves at once.  A count goes back to 0 by the increment that completes
+// it, not by a store: also where two norms of a list overlap, against the rule, every count is 0
+// when both have ended, and the list's next norm is right.
+__device__ __forceinline__ bool count_self(uint32_t* ticket, uint32_t all) {
+  return atomicInc(ticket, all - 1) == all - 1;  // device scope, relaxed
 }
 __global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
   __shared__ double red[4], red_all[4];
@@ -226,13 +228,9 @@ __global__ __launch_bounds__(256) void k_grad_norm(GradArgs a) {
       if (!few) {
         const unsigned mine = blockIdx.x % kTickets;
         uint32_t* ticket = a.tickets + (1 + mine) * (kLine / 4);
-        done = count_self(ticket) == (grid - mine - 1) / kTickets;
-        if (done) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        done = count_self(ticket, (grid - mine - 1) / kTickets + 1);
       }
-      if (done) {
-        done = count_self(a.tickets) == (few ? grid : unsigned(kTickets)) - 1;
-        if (done) __hip_atomic_store(a.tickets, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
+      if (done) done = count_self(a.tickets, few ? grid : unsigned(kTickets));
       last = done;
     }
     __syncthreads();

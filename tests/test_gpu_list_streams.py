@@ -120,3 +120,24 @@ def test_norms_of_one_list_on_branches_of_a_capture():
         assert all(torch.equal(out, eager) for out in outs) and norm_close(eager, want)
         for x in views:
             x.mul_(0.5)
+
+
+@pytest.mark.parametrize("spec", ["long", "tails"])  # counted in groups, and by one count
+def test_overlapping_norms_leave_the_list_usable(spec):
+    """Through the library, which orders nothing: the values of norms that overlap are undefined,
+    but the next ones, after a synchronisation, are right."""
+    log(f"overlapping norms, {spec}")
+    views, _ = make(LISTS[spec], 104, std=1.0)
+    want = grad_norm([to64(x) for x in views])
+    lst = nm.GradClip(views)
+    outs = torch.zeros(8, device=DEV)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k in range(8):
+            rc = nm.lib().muon_grad_norm(ctypes.byref(lst.list), 0, ctypes.c_void_p(outs.data_ptr() + 4 * k),
+                                         ctypes.c_void_p(streams[k % 4].cuda_stream))
+            assert rc == nm.MUON_OK
+        torch.cuda.synchronize()
+        assert norm_close(lst.norm(), want) and norm_close(lst.norm(), want)
+        torch.cuda.synchronize()
