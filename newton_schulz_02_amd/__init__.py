@@ -445,6 +445,7 @@ class MuonStep:
         _check(lib().muon_step_clipped(self.arr, self.count, ctypes.byref(self.hp), _clip_arg(clip, self.device),
                                        c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
                                        _stream_handle(stream, self.device)))
+        _keep_for(clip[0], stream, self.device)
 
     def check(self, stream=None) -> None:
         """Raise MuonError if the last step reported a failure (muon_workspace_check)."""
@@ -815,6 +816,19 @@ def _clip_arg(clip, device):
     return ctypes.byref(muon_clip(_norm_arg(norm, device), float(max_norm), 0))
 
 
+def _stream_of(stream, device):
+    import torch
+
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device)
+
+
+def _keep_for(tensor, stream, device) -> None:
+    """A call on a stream that the caller names reads or writes `tensor` when that stream gets
+    there: the allocator gives its memory to nobody before."""
+    if stream is not None:
+        tensor.record_stream(_stream_of(stream, device))
+
+
 def _capture_of(handle: int) -> int:
     """The identity of the graph capture that a stream takes part in, 0 for none."""
     out = c_uint64(0)
@@ -858,7 +872,7 @@ class _List:
 
         if stream is None:
             return torch.cuda.current_stream(self.device)
-        return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), self.device)
+        return _stream_of(stream, self.device)
 
     def _handle(self, stream):
         """The handle of the stream of a call, which may use the list."""
@@ -905,7 +919,9 @@ class GradClip(_List):
     after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
     `stream` (default: the current one) at construction; calls on other streams wait for it.
     Inside a graph capture it is recorded, and only calls on streams of that capture can use it.
-    Norms on several streams run in the order of the calls.  Replays of graphs are not calls:
+    Norms on several streams run in the order of the calls.  A norm that is passed or written on
+    a named stream may be dropped after the call; the gradients are kept by this object alone.
+    Replays of graphs are not calls:
     graphs that hold norms of one list are replayed one after another (and after eager norms of
     it), or each has a list of its own."""
 
@@ -953,6 +969,7 @@ class GradClip(_List):
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
         self._call_norm(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
+        _keep_for(out, stream, self.device)
         return out
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
@@ -960,6 +977,7 @@ class GradClip(_List):
         device tensor, for example one that was reduced over ranks."""
         handle = self._handle(stream)
         self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream, handle)
+        _keep_for(norm, stream, self.device)
 
     def clip_norm(self, max_norm, kind="l2", *, out=None, stream=None):
         """norm(), then clip() by it; returns the norm from before."""
@@ -967,6 +985,7 @@ class GradClip(_List):
         out = self._out(out, stream)
         self._call_norm(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream,
                         handle)
+        _keep_for(out, stream, self.device)
         return out
 
 
@@ -997,6 +1016,8 @@ class AdamWStep(_List):
             self.hp.lr = float(lr)
         arg = None if clip is None else _clip_arg(clip, self.device)
         self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream, handle)
+        if clip is not None:
+            _keep_for(clip[0], stream, self.device)
 
 
 def grad_norm(grads, kind="l2", *, device=None, stream=None):

@@ -141,3 +141,41 @@ def test_overlapping_norms_leave_the_list_usable(spec):
         torch.cuda.synchronize()
         assert norm_close(lst.norm(), want) and norm_close(lst.norm(), want)
         torch.cuda.synchronize()
+
+
+def busy(stream):
+    """Queue some 20 ms of work on a stream."""
+    with torch.cuda.stream(stream):
+        a = torch.ones(4096, 4096, device=DEV)
+        for _ in range(30):
+            a = a @ a * 2.0 ** -12
+    return a
+
+
+def places(numel, dtype, count=64):
+    """Addresses that the allocator gives tensors of the current stream now; nothing is written."""
+    return {t.data_ptr() for t in [torch.empty(numel, dtype=dtype, device=DEV) for _ in range(count)]}
+
+
+def test_a_dropped_norm_stays_until_its_named_stream_has_read_it():
+    """clip=(norm, limit) on a side stream that is still busy, the norm dropped at once: its
+    memory is not given away before the side stream gets there."""
+    log("norm dropped while a stream is busy")
+    views, _ = make([(5000, torch.float32)], 105, std=1.0)
+    p, m, v = ([torch.zeros(5000, device=DEV)] for _ in range(3))
+    w, g, mom = (torch.zeros(64, 64, device=DEV) for _ in range(3))
+    lst, adam, muon = nm.GradClip(views), nm.AdamWStep(p, views, m, v), nm.MuonStep([w], [g], [mom])
+    side = torch.cuda.Stream()
+    calls = [lambda n: adam(1, clip=(n, 1.0), stream=side), lambda n: lst.clip(n, 1.0, stream=side),
+             lambda n: muon(side, clip=(n, 1.0)), lambda n: lst.norm(out=n, stream=side)]
+    for call in calls:
+        norm = torch.full((), 2.0, device=DEV)
+        at = norm.data_ptr()
+        torch.cuda.synchronize()
+        keep = busy(side)
+        call(norm)
+        del norm
+        assert at not in places((), torch.float32)
+        assert not side.query()  # the side stream was still busy
+        side.synchronize()
+        del keep

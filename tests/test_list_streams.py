@@ -159,6 +159,41 @@ def test_a_branch_waits_for_a_norm_that_its_origin_captured(streams):
     assert waited(b, lst) == [1]
 
 
+class Value:
+    """Stands in for a norm on the device."""
+
+    def __init__(self):
+        self.dtype, self.device, self.kept = torch.float32, torch.device("cuda", 0), []
+
+    def numel(self):
+        return 1
+
+    def data_ptr(self):
+        return 1 << 30
+
+    def record_stream(self, stream):
+        self.kept.append(stream.cuda_stream)
+
+
+@pytest.mark.parametrize("call", ["norm", "clip", "clip_norm", "adamw", "muon"])
+def test_a_norm_used_on_a_named_stream_is_kept_until_then(streams, monkeypatch, call):
+    ok = types.SimpleNamespace(**{name: lambda *a: nm.MUON_OK for name in (
+        "muon_grad_norm", "muon_grad_clip", "muon_grad_clip_norm", "adamw_list_step", "muon_step_clipped")})
+    monkeypatch.setattr(nm, "lib", lambda: ok)
+    a, b = streams(1), streams(2)
+    grads, adam, muon = laid_out(a), laid_out(a, nm.AdamWStep), object.__new__(nm.MuonStep)
+    adam.hp = nm.adamw_hparams()
+    muon.arr, muon.count, muon.hp, muon.device = None, 0, nm.make_hparams(), torch.device("cuda", 0)
+    muon.workspace = torch.zeros(1)
+    run = {"norm": lambda x, s: grads.norm(out=x, stream=s), "clip": lambda x, s: grads.clip(x, 1.0, stream=s),
+           "clip_norm": lambda x, s: grads.clip_norm(1.0, out=x, stream=s),
+           "adamw": lambda x, s: adam(1, clip=(x, 1.0), stream=s), "muon": lambda x, s: muon(s, clip=(x, 1.0))}[call]
+    for stream in (a, b):
+        x = Value()
+        run(x, stream)
+        assert x.kept == [stream.cuda_stream]
+
+
 def test_stream_capture_arguments():
     out = ctypes.c_uint64(5)
     assert nm.lib().muon_stream_capture(None, None) == nm.MUON_EINVAL
