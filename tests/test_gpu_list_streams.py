@@ -179,3 +179,21 @@ def test_a_dropped_norm_stays_until_its_named_stream_has_read_it():
         assert not side.query()  # the side stream was still busy
         side.synchronize()
         del keep
+
+
+def test_a_dropped_list_keeps_its_workspace_until_its_streams_have_passed():
+    log("list dropped while a stream is busy")
+    views, _ = make(LISTS["tails"], 106, std=1.0)
+    want = grad_norm([to64(x) for x in views])
+    lst = nm.GradClip(views)
+    at, size = lst.workspace.data_ptr(), lst.workspace.numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    keep = busy(side)
+    norm = lst.norm(stream=side)
+    del lst
+    assert at not in places(size, torch.uint8)
+    assert not side.query()
+    side.synchronize()
+    assert norm_close(norm, want)
+    del keep
