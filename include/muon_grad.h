@@ -29,6 +29,9 @@
  * to fp32 once (inf above the fp32 range).  c and its product with g are fp32; a bf16
  * gradient is rounded (to nearest even) once, on store.  AdamW runs in fp32, and a bf16 param
  * is rounded once.  Without a master that rounding loses updates below half a bf16 step.
+ * The betas of adamw_hparams are floats, and are taken as what they are: 0.9999f is
+ * 0.99989998.., so 1 - 0.9999f, and v with it, is 1.7e-4 off what 0.9999 gives.  The _double
+ * entry points take 64-bit hyperparameters; m and v then follow the betas given.
  *
  * Lists: a list is laid out once (muon_grad_list_init, adamw_list_init: the tensors'
  * addresses and sizes, and a map of their parts, go to the caller's workspace) and then used
@@ -125,9 +128,27 @@ int muon_grad_clip(const muon_grad_list* list, const muon_clip* clip, void* hip_
 /* muon_grad_norm, then muon_grad_clip by its result. */
 int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm, float* norm, void* hip_stream);
 
+/* Hyperparameters of AdamW in 64 bits: lr, eps and weight_decay are rounded to fp32, the betas,
+ * in [0, 1), are not (nor 1 - beta). */
+typedef struct adamw_hparams_double {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int32_t step;
+  int32_t reserved; /* must be 0 */
+} adamw_hparams_double;
+
+/* adamw_step (muon.h) with 64-bit hyperparameters. */
+int adamw_step_double(float* p, const float* g, float* m, float* v, int64_t n, const adamw_hparams_double* hp,
+                      void* hip_stream);
+
 /* AdamW over the list.  hp as adamw_step; clip may be NULL (no clipping), and clip->norm is no
  * part of a tensor that the list updates. */
 int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream);
+int adamw_list_step_double(const adamw_list* list, const adamw_hparams_double* hp, const muon_clip* clip,
+                           void* hip_stream);
 
 /* muon_step whose gradients are scaled by the coefficient of `clip` as the momentum reads
  * them: M <- beta M + c G, in fp32, the gradients unchanged.  clip NULL is muon_step;

@@ -79,6 +79,11 @@ class shampoo_hparams(ctypes.Structure):
     _fields_ = [("lr", c_float), ("beta2", c_float), ("eps", c_float), ("root_iters", c_int32)]
 
 
+class adamw_hparams_double(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("weight_decay", c_double), ("step", c_int32), ("reserved", c_int32)]
+
+
 class muon_grad(ctypes.Structure):
     _fields_ = [("grad", c_void_p), ("n", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
 
@@ -109,6 +114,8 @@ _SIGNATURES = {
     "muon_workspace_size": (c_int, [_MATP, c_int32, _HPP, POINTER(c_size_t)]),
     "muon_step": (c_int, [_MATP, c_int32, _HPP, c_void_p, c_size_t, c_void_p]),
     "adamw_step": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, POINTER(adamw_hparams), c_void_p]),
+    "adamw_step_double": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, POINTER(adamw_hparams_double),
+                                  c_void_p]),
     "muon_step_cost": (c_int, [_MATP, c_int32, _HPP, POINTER(c_double), POINTER(c_double)]),
     "muon_plan_describe": (c_int, [_MATP, c_int32, _HPP, c_char_p, c_size_t]),
     "muon_profile_begin": (c_int, []),
@@ -148,6 +155,7 @@ _SIGNATURES = {
     "adamw_list_size": (c_int, [POINTER(adamw_tensor), c_int32, POINTER(c_size_t)]),
     "adamw_list_init": (c_int, [POINTER(adamw_tensor), c_int32, c_void_p, c_size_t, c_void_p, POINTER(adamw_list)]),
     "adamw_list_step": (c_int, [POINTER(adamw_list), POINTER(adamw_hparams), POINTER(muon_clip), c_void_p]),
+    "adamw_list_step_double": (c_int, [POINTER(adamw_list), POINTER(adamw_hparams_double), POINTER(muon_clip), c_void_p]),
 }
 
 _lib = None
@@ -525,10 +533,10 @@ def adamw_step(p, g, m, v, *, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_d
             raise ValueError("adamw tensors must be contiguous float32")
         if t.numel() != p.numel():
             raise ValueError("adamw tensors must have the same size")
-    hp = adamw_hparams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step))
-    _check(lib().adamw_step(c_void_p(p.data_ptr()), c_void_p(g.data_ptr()), c_void_p(m.data_ptr()),
-                            c_void_p(v.data_ptr()), p.numel(), ctypes.byref(hp),
-                            _stream_handle(stream, p.device)))
+    hp = adamw_hparams_double(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), int(step), 0)
+    _check(lib().adamw_step_double(c_void_p(p.data_ptr()), c_void_p(g.data_ptr()), c_void_p(m.data_ptr()),
+                                   c_void_p(v.data_ptr()), p.numel(), ctypes.byref(hp),
+                                   _stream_handle(stream, p.device)))
 
 
 def tile_order(tri: bool, tm: int, tn: int = 0):
@@ -1002,7 +1010,7 @@ class AdamWStep(_List):
                  weight_decay=0.1, device=None, workspace=None, stream=None):
         self.params, self.grads, self.ms, self.vs = list(params), list(grads), list(ms), list(vs)
         self.masters = None if masters is None else list(masters)
-        self.hp = adamw_hparams(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 1)
+        self.hp = adamw_hparams_double(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), 1, 0)
         arr = adamw_array(self.params, self.grads, self.ms, self.vs, self.masters, decays)
         tensors = self.params + self.grads + self.ms + self.vs + [w for w in self.masters or [] if w is not None]
         self._lay_out(arr, len(self.params), tensors, device, workspace, stream)
@@ -1015,7 +1023,7 @@ class AdamWStep(_List):
         if lr is not None:
             self.hp.lr = float(lr)
         arg = None if clip is None else _clip_arg(clip, self.device)
-        self._call(lib().adamw_list_step, (ctypes.byref(self.hp), arg), stream, handle)
+        self._call(lib().adamw_list_step_double, (ctypes.byref(self.hp), arg), stream, handle)
         if clip is not None:
             _keep_for(clip[0], stream, self.device)
 

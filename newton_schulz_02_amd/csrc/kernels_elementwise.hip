@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void k_norm(NormArgs a) {
     for (int i = threadIdx.x; i < a.split_cnt_n; i += 256) a.split_cnt[i] = 0;
 }
 
-__global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
+__global__ __launch_bounds__(256) void k_adamw(AdamArgs a, AdamBetas b) {
   const int64_t stride = int64_t(gridDim.x) * 256 * 4;
   const bool vec = ((reinterpret_cast<uintptr_t>(a.p) | reinterpret_cast<uintptr_t>(a.g) |
                      reinterpret_cast<uintptr_t>(a.m) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0;
@@ -218,17 +218,17 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
       const float4 g = *reinterpret_cast<const float4*>(a.g + i);
       float4 m = *reinterpret_cast<const float4*>(a.m + i);
       float4 v = *reinterpret_cast<const float4*>(a.v + i);
-      adamw_one(p.x, g.x, m.x, v.x, a, a.wd);
-      adamw_one(p.y, g.y, m.y, v.y, a, a.wd);
-      adamw_one(p.z, g.z, m.z, v.z, a, a.wd);
-      adamw_one(p.w, g.w, m.w, v.w, a, a.wd);
+      adamw_one(p.x, g.x, m.x, v.x, a, b, a.wd);
+      adamw_one(p.y, g.y, m.y, v.y, a, b, a.wd);
+      adamw_one(p.z, g.z, m.z, v.z, a, b, a.wd);
+      adamw_one(p.w, g.w, m.w, v.w, a, b, a.wd);
       *reinterpret_cast<float4*>(a.p + i) = p;
       *reinterpret_cast<float4*>(a.m + i) = m;
       *reinterpret_cast<float4*>(a.v + i) = v;
     } else {
       for (int64_t j = i; j < i + 4 && j < a.n; ++j) {
         float p = a.p[j], m = a.m[j], v = a.v[j];
-        adamw_one(p, a.g[j], m, v, a, a.wd);
+        adamw_one(p, a.g[j], m, v, a, b, a.wd);
         a.p[j] = p;
         a.m[j] = m;
         a.v[j] = v;
@@ -261,12 +261,16 @@ int muon_launch_norm(const NormArgs& a, void* stream) {
   return hipGetLastError();
 }
 
-int muon_launch_adamw(const AdamArgs& a, void* stream) {
+int muon_launch_adamw(const AdamArgs& a, const AdamBetas& b, void* stream) {
   if (a.n <= 0) return hipSuccess;
   const int64_t per_block = 256 * 4;
   int64_t blocks = (a.n + per_block - 1) / per_block;
   if (blocks > 256 * 64) blocks = 256 * 64;
   hipLaunchKernelGGL(k_adamw, dim3(unsigned(blocks)), dim3(256), 0,
-                     static_cast<hipStream_t>(stream), a);
+                     static_cast<hipStream_t>(stream), a, b);
   return hipGetLastError();
+}
+
+int muon_launch_adamw(const AdamArgs& a, void* stream) {
+  return muon_launch_adamw(a, {{a.beta1, 0.0f, 1.0f - a.beta1}, {a.beta2, 0.0f, 1.0f - a.beta2}}, stream);
 }

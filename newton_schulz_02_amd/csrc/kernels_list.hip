@@ -331,7 +331,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
     for (int u = 0; u < U; ++u) {
       const int i = (u * 256 + tid) * 4;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, wd);
+      for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, a.betas, wd);
       store4(m + i, ms[u]);
       store4(v + i, vs[u]);
       store4(x + i, xs[u]);
@@ -361,7 +361,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
     load4(v + i, vs[u]);
   }
   if (e >= 0) {
-    adamw_one(xe, coef * ge, me, ve, a, wd);
+    adamw_one(xe, coef * ge, me, ve, a, a.betas, wd);
     m[e] = me;
     v[e] = ve;
     st_f(x + e, xe);
@@ -372,7 +372,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamRec& r, uint32_t c, float 
     const int i = (u * 256 + tid) * 4;
     if (i < lo || i + 4 > hi) continue;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, wd);
+    for (int k = 0; k < 4; ++k) adamw_one(xs[u][k], coef * gs[u][k], ms[u][k], vs[u][k], a, a.betas, wd);
     store4(m + i, ms[u]);
     store4(v + i, vs[u]);
     store4(x + i, xs[u]);

@@ -8,11 +8,18 @@
 
 namespace muon {
 
-// One element of AdamW in fp32; A holds lr, beta1, beta2, eps and the bias corrections.
+// beta x + add, for a state x.  lo is 0 where beta is a float: its product is left out then, as
+// it would make a NaN of an infinite state.
+__device__ __forceinline__ float decayed(const AdamBeta& b, float x, float add) {
+  return fmaf(b.hi, x, b.lo != 0.0f ? fmaf(b.lo, x, add) : add);
+}
+
+// One element of AdamW in fp32; A holds lr, eps and the bias corrections.
 template <typename A>
-__device__ __forceinline__ void adamw_one(float& p, float g, float& m, float& v, const A& a, float wd) {
-  m = fmaf(a.beta1, m, (1.0f - a.beta1) * g);
-  v = fmaf(a.beta2, v, (1.0f - a.beta2) * g * g);
+__device__ __forceinline__ void adamw_one(float& p, float g, float& m, float& v, const A& a, const AdamBetas& b,
+                                          float wd) {
+  m = decayed(b.b1, m, b.b1.rest * g);
+  v = decayed(b.b2, v, b.b2.rest * g * g);
   const float mh = m / a.bc1;
   const float vh = v / a.bc2;
   p = p - a.lr * (mh / (sqrtf(vh) + a.eps) + wd * p);

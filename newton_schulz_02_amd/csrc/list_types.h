@@ -14,6 +14,17 @@ struct ClipArg {
   float max_norm;
 };
 
+// A decay rate of AdamW's state as the kernels use it: beta = hi + lo, hi being the largest
+// float that is not above it, and rest = 1 - beta, rounded once from 64 bits.  One float of beta
+// is not enough: 1 - 0.9999f is off by 1.7e-4 of itself, and so would v be, after one step with
+// a rounded beta's own difference from 1, after many with the true one.
+struct AdamBeta {
+  float hi, lo, rest;
+};
+struct AdamBetas {
+  AdamBeta b1, b2;
+};
+
 constexpr int64_t kLine = 128;         // gradient chunks start on multiples of this address
 constexpr int kTickets = 8;            // groups in which a norm's workgroups count themselves
 constexpr int64_t kListTickets = 256;  // a list's workspace: status word, counts, entries
@@ -60,7 +71,8 @@ struct AdamListArgs {
   const uint32_t* map;  // tensor of each chunk
   uint32_t chunks;
   ClipArg clip;
-  float lr, beta1, beta2, eps, wd;
+  AdamBetas betas;
+  float lr, eps, wd;
   float bc1, bc2;
 };
 
@@ -72,5 +84,7 @@ int muon_launch_adamw_map(const muon::AdamRec* recs, int count, uint32_t chunks,
 int muon_launch_grad_norm(const muon::GradArgs& a, void* stream);
 int muon_launch_grad_clip(const muon::GradArgs& a, void* stream);
 int muon_launch_adamw_list(const muon::AdamListArgs& a, void* stream);
+// muon_launch_adamw with betas in more than fp32 (a.beta1 and a.beta2 are not read).
+int muon_launch_adamw(const muon::AdamArgs& a, const muon::AdamBetas& b, void* stream);
 // muon_launch_momentum with G scaled by the coefficient of `clip` (its norm is not null).
 int muon_launch_momentum_clipped(const muon::MomArgs& a, const muon::ClipArg& clip, int dtype, void* stream);

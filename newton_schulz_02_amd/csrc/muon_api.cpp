@@ -259,15 +259,39 @@ int run_launch(int dev, hipStream_t s, const Plan& plan, const PlanLaunch& L, in
                [&] { return muon_launch_gemm(a, L.dtype, s); });
 }
 
-int check_adamw(const adamw_hparams* hp) {
-  if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
-  const float fs[] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay};
-  for (float f : fs)
-    if (!std::isfinite(f)) return fail(MUON_EINVAL, "non-finite hyperparameter");
-  if (hp->step < 1) return fail(MUON_EINVAL, "step must be >= 1");
-  if (hp->beta1 < 0.0f || hp->beta1 >= 1.0f || hp->beta2 < 0.0f || hp->beta2 >= 1.0f)
+adamw_hparams_double widen(const adamw_hparams& hp) {
+  return {hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, hp.step, 0};
+}
+
+int check_adamw(const adamw_hparams_double& hp) {
+  const double fs[] = {hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay};
+  for (double f : fs)
+    if (!std::isfinite(float(f))) return fail(MUON_EINVAL, "non-finite hyperparameter");
+  if (hp.step < 1) return fail(MUON_EINVAL, "step must be >= 1");
+  if (hp.beta1 < 0.0 || hp.beta1 >= 1.0 || hp.beta2 < 0.0 || hp.beta2 >= 1.0)
     return fail(MUON_EINVAL, "beta1/beta2 outside [0, 1)");
+  if (hp.reserved != 0) return fail(MUON_EINVAL, "hparams: reserved field must be 0");
   return MUON_OK;
+}
+
+AdamBeta split_beta(double beta) {
+  AdamBeta b;
+  b.hi = float(beta);
+  if (double(b.hi) > beta) b.hi = std::nextafterf(b.hi, 0.0f);
+  b.lo = float(beta - double(b.hi));
+  b.rest = float(1.0 - beta);
+  return b;
+}
+
+// What every AdamW kernel takes of the hyperparameters; A has lr, eps, wd, bc1 and bc2.
+template <typename A>
+AdamBetas set_adamw(A* a, const adamw_hparams_double& hp) {
+  a->lr = float(hp.lr);
+  a->eps = float(hp.eps);
+  a->wd = float(hp.weight_decay);
+  a->bc1 = float(1.0 - std::pow(hp.beta1, double(hp.step)));
+  a->bc2 = float(1.0 - std::pow(hp.beta2, double(hp.step)));
+  return {split_beta(hp.beta1), split_beta(hp.beta2)};
 }
 
 int check_max_norm(float max_norm) {
@@ -896,41 +920,63 @@ int muon_tune_import(const char* text) {
   return MUON_OK;
 }
 
+namespace {
+// betas null: those of `a`.
+int run_adamw(float* p, const float* g, float* m, float* v, int64_t n, AdamArgs a, const AdamBetas* betas,
+              void* hip_stream) {
+  if (n < 0) return fail(MUON_EINVAL, "n is negative");
+  if (n == 0) return MUON_OK;
+  if (!p || !g || !m || !v) return fail(MUON_EINVAL, "NULL pointer");
+  const uintptr_t ptrs[4] = {(uintptr_t)p, (uintptr_t)g, (uintptr_t)m, (uintptr_t)v};
+  for (uintptr_t x : ptrs)
+    if (x % 4) return fail(MUON_EINVAL, "pointer not 4-byte aligned");
+  const uintptr_t bytes = uintptr_t(n) * 4;
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (ptrs[i] < ptrs[j] + bytes && ptrs[j] < ptrs[i] + bytes)
+        return fail(MUON_EALIAS, "AdamW buffers overlap");
+  a.p = p;
+  a.g = g;
+  a.m = m;
+  a.v = v;
+  a.n = n;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0, rc;
+  if ((rc = current_device(&dev)) != MUON_OK) return rc;
+  if ((rc = check_device(dev)) != MUON_OK) return rc;
+  return timed(dev, s, "adamw", 0.0, 28.0 * double(n),
+               [&] { return betas ? muon_launch_adamw(a, *betas, s) : muon_launch_adamw(a, s); });
+}
+}  // namespace
+
 int adamw_step(float* p, const float* g, float* m, float* v, int64_t n, const adamw_hparams* hp,
                void* hip_stream) {
   try {
-    const int bad = check_adamw(hp);
+    if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+    const int bad = check_adamw(widen(*hp));
     if (bad != MUON_OK) return bad;
-    if (n < 0) return fail(MUON_EINVAL, "n is negative");
-    if (n == 0) return MUON_OK;
-    if (!p || !g || !m || !v) return fail(MUON_EINVAL, "NULL pointer");
-    const uintptr_t ptrs[4] = {(uintptr_t)p, (uintptr_t)g, (uintptr_t)m, (uintptr_t)v};
-    for (uintptr_t x : ptrs)
-      if (x % 4) return fail(MUON_EINVAL, "pointer not 4-byte aligned");
-    const uintptr_t bytes = uintptr_t(n) * 4;
-    for (int i = 0; i < 4; ++i)
-      for (int j = i + 1; j < 4; ++j)
-        if (ptrs[i] < ptrs[j] + bytes && ptrs[j] < ptrs[i] + bytes)
-          return fail(MUON_EALIAS, "AdamW buffers overlap");
     AdamArgs a;
-    a.p = p;
-    a.g = g;
-    a.m = m;
-    a.v = v;
-    a.n = n;
-    a.lr = hp->lr;
+    std::memset(&a, 0, sizeof a);
+    set_adamw(&a, widen(*hp));
     a.beta1 = hp->beta1;
     a.beta2 = hp->beta2;
-    a.eps = hp->eps;
-    a.wd = hp->weight_decay;
-    a.bc1 = float(1.0 - std::pow(double(hp->beta1), double(hp->step)));
-    a.bc2 = float(1.0 - std::pow(double(hp->beta2), double(hp->step)));
-    hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    std::lock_guard<std::mutex> lock(g_mu);
-    int dev = 0, rc;
-    if ((rc = current_device(&dev)) != MUON_OK) return rc;
-    if ((rc = check_device(dev)) != MUON_OK) return rc;
-    return timed(dev, s, "adamw", 0.0, 28.0 * double(n), [&] { return muon_launch_adamw(a, s); });
+    return run_adamw(p, g, m, v, n, a, nullptr, hip_stream);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int adamw_step_double(float* p, const float* g, float* m, float* v, int64_t n, const adamw_hparams_double* hp,
+                      void* hip_stream) {
+  try {
+    if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+    const int bad = check_adamw(*hp);
+    if (bad != MUON_OK) return bad;
+    AdamArgs a;
+    std::memset(&a, 0, sizeof a);
+    const AdamBetas b = set_adamw(&a, *hp);
+    return run_adamw(p, g, m, v, n, a, &b, hip_stream);
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }
@@ -1175,31 +1221,42 @@ int muon_grad_clip_norm(const muon_grad_list* list, int32_t kind, float max_norm
   }
 }
 
+namespace {
+int run_adamw_list(const adamw_list* list, const adamw_hparams_double& hp, const muon_clip* clip, void* hip_stream) {
+  ListHandle h;
+  int rc, dev = 0;
+  if ((rc = open_list(list, kAdamListMagic, &h)) != MUON_OK) return rc;
+  if ((rc = check_adamw(hp)) != MUON_OK) return rc;
+  if (clip && ((rc = check_clip(clip)) != MUON_OK || (rc = check_norm_place(h, clip->norm)) != MUON_OK)) return rc;
+  AdamListArgs a;
+  std::memset(&a, 0, sizeof a);
+  const char* ws = reinterpret_cast<const char*>(uintptr_t(h.workspace));
+  a.recs = reinterpret_cast<const AdamRec*>(ws + kListHead);
+  a.map = reinterpret_cast<const uint32_t*>(ws + h.map_off);
+  a.chunks = h.chunks;
+  if (clip) a.clip = {clip->norm, clip->max_norm};
+  a.betas = set_adamw(&a, hp);
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  std::lock_guard<std::mutex> lock(g_mu);
+  if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
+  return timed(dev, s, "adamw_list", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_adamw_list(a, s); });
+}
+}  // namespace
+
 int adamw_list_step(const adamw_list* list, const adamw_hparams* hp, const muon_clip* clip, void* hip_stream) {
   try {
-    ListHandle h;
-    int rc, dev = 0;
-    if ((rc = open_list(list, kAdamListMagic, &h)) != MUON_OK) return rc;
-    if ((rc = check_adamw(hp)) != MUON_OK) return rc;
-    if (clip && ((rc = check_clip(clip)) != MUON_OK || (rc = check_norm_place(h, clip->norm)) != MUON_OK)) return rc;
-    AdamListArgs a;
-    std::memset(&a, 0, sizeof a);
-    const char* ws = reinterpret_cast<const char*>(uintptr_t(h.workspace));
-    a.recs = reinterpret_cast<const AdamRec*>(ws + kListHead);
-    a.map = reinterpret_cast<const uint32_t*>(ws + h.map_off);
-    a.chunks = h.chunks;
-    if (clip) a.clip = {clip->norm, clip->max_norm};
-    a.lr = hp->lr;
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.eps = hp->eps;
-    a.wd = hp->weight_decay;
-    a.bc1 = float(1.0 - std::pow(double(hp->beta1), double(hp->step)));
-    a.bc2 = float(1.0 - std::pow(double(hp->beta2), double(hp->step)));
-    hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    std::lock_guard<std::mutex> lock(g_mu);
-    if ((rc = check_list_place(h, s, &dev)) != MUON_OK) return rc;
-    return timed(dev, s, "adamw_list", 0.0, h.read_bytes + h.write_bytes, [&] { return muon_launch_adamw_list(a, s); });
+    if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+    return run_adamw_list(list, widen(*hp), clip, hip_stream);
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
+}
+
+int adamw_list_step_double(const adamw_list* list, const adamw_hparams_double* hp, const muon_clip* clip,
+                           void* hip_stream) {
+  try {
+    if (!hp) return fail(MUON_EINVAL, "hparams is NULL");
+    return run_adamw_list(list, *hp, clip, hip_stream);
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }

@@ -178,11 +178,11 @@ class Value:
 @pytest.mark.parametrize("call", ["norm", "clip", "clip_norm", "adamw", "muon"])
 def test_a_norm_used_on_a_named_stream_is_kept_until_then(streams, monkeypatch, call):
     ok = types.SimpleNamespace(**{name: lambda *a: nm.MUON_OK for name in (
-        "muon_grad_norm", "muon_grad_clip", "muon_grad_clip_norm", "adamw_list_step", "muon_step_clipped")})
+        "muon_grad_norm", "muon_grad_clip", "muon_grad_clip_norm", "adamw_list_step_double", "muon_step_clipped")})
     monkeypatch.setattr(nm, "lib", lambda: ok)
     a, b = streams(1), streams(2)
     grads, adam, muon = laid_out(a), laid_out(a, nm.AdamWStep), object.__new__(nm.MuonStep)
-    adam.hp = nm.adamw_hparams()
+    adam.hp = nm.adamw_hparams_double()
     muon.arr, muon.count, muon.hp, muon.device = None, 0, nm.make_hparams(), torch.device("cuda", 0)
     muon.workspace = torch.zeros(1)
     run = {"norm": lambda x, s: grads.norm(out=x, stream=s), "clip": lambda x, s: grads.clip(x, 1.0, stream=s),
