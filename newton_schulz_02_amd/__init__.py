@@ -262,6 +262,15 @@ def _stream_handle(stream, device):
     return c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _check_workspace(workspace, need: int) -> None:
+    """A caller's workspace tensor holds `need` bytes one behind the other (an expanded one has
+    more elements than memory)."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
+
+
 # --- entry points -----------------------------------------------------------------------
 
 def workspace_size_raw(arr, count: int, hp: muon_hparams) -> int:
@@ -436,8 +445,7 @@ class MuonStep:
         self.device = self.params[0].device if self.count else torch.device("cuda")
         if workspace is None:
             workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
-        if workspace.numel() < self.ws_bytes:
-            raise ValueError(f"workspace has {workspace.numel()} bytes, needs {self.ws_bytes}")
+        _check_workspace(workspace, self.ws_bytes)
         self.workspace = workspace
 
     def cost(self) -> tuple[float, float]:
@@ -700,8 +708,7 @@ class ShampooStep:
         self.device = self.params[0].device if self.count else torch.device("cuda")
         if workspace is None:
             workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
-        if workspace.numel() < self.ws_bytes:
-            raise ValueError(f"workspace has {workspace.numel()} bytes, needs {self.ws_bytes}")
+        _check_workspace(workspace, self.ws_bytes)
         self.workspace = workspace
 
     def check(self, stream=None) -> None:
@@ -862,8 +869,7 @@ class _List:
         with torch.cuda.device(self.device), torch.cuda.stream(home):
             if workspace is None:
                 workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
-            if workspace.numel() < self.ws_bytes:
-                raise ValueError(f"workspace has {workspace.numel()} bytes, needs {self.ws_bytes}")
+            _check_workspace(workspace, self.ws_bytes)
             if workspace.device != self.device:
                 raise ValueError(f"workspace is on {workspace.device}, the list on {self.device}")
             self.workspace = workspace

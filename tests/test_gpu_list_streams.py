@@ -197,3 +197,14 @@ def test_a_dropped_list_keeps_its_workspace_until_its_streams_have_passed():
     side.synchronize()
     assert norm_close(norm, want)
     del keep
+
+
+def test_an_expanded_workspace_is_refused():
+    log("expanded workspace")
+    g = torch.ones(10, device=DEV)
+    for bad in (torch.zeros(1, dtype=torch.uint8, device=DEV).expand(1 << 20),
+                torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            nm.GradClip([g], workspace=bad)
+        with pytest.raises(ValueError, match="contiguous"):
+            nm.AdamWStep([g], [g.clone()], [g.clone()], [g.clone()], workspace=bad)
