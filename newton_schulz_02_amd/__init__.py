@@ -886,7 +886,10 @@ class _List:
 
         if stream is None:
             return torch.cuda.current_stream(self.device)
-        return _stream_of(stream, self.device)
+        stream = _stream_of(stream, self.device)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the list on {self.device}")
+        return stream
 
     def _handle(self, stream):
         """The handle of the stream of a call, which may use the list."""

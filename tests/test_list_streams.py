@@ -194,6 +194,16 @@ def test_a_norm_used_on_a_named_stream_is_kept_until_then(streams, monkeypatch, 
         assert x.kept == [stream.cuda_stream]
 
 
+def test_a_stream_of_another_device_is_refused(streams):
+    a, b = streams(1), streams(2)
+    b.device = torch.device("cuda", 1)
+    lst = laid_out(a)
+    for call in (lambda: use(lst, b), lambda: norm(lst, b)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
+    assert not b.waits
+
+
 def test_stream_capture_arguments():
     out = ctypes.c_uint64(5)
     assert nm.lib().muon_stream_capture(None, None) == nm.MUON_EINVAL
