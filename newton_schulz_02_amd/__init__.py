@@ -981,8 +981,8 @@ class GradClip(_List):
         self._norm_last, self._norm_streams = stream.cuda_stream, still
 
     def norm(self, kind="l2", *, out=None, stream=None):
-        """The norm of all gradients, as a float32 device tensor (`out`, or a new one that
-        belongs to the stream of the call)."""
+        """The norm of all gradients, as a float32 device tensor (`out`, which is no part of a
+        gradient, or a new one that belongs to the stream of the call)."""
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
         self._call_norm(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
@@ -991,7 +991,7 @@ class GradClip(_List):
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
         """Scale the gradients in place by min(1, max_norm / (norm + 1e-6)); `norm` is a float32
-        device tensor, for example one that was reduced over ranks."""
+        device tensor, for example one that was reduced over ranks, and no part of a gradient."""
         handle = self._handle(stream)
         self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream, handle)
         _keep_for(norm, stream, self.device)
@@ -1026,13 +1026,19 @@ class AdamWStep(_List):
 
     def __call__(self, step, *, lr=None, clip=None, stream=None) -> None:
         """Update number `step` (>= 1), with `lr` from now on if given; clip = (norm, max_norm)
-        scales the gradients by min(1, max_norm / (norm + 1e-6)) as they are read."""
+        scales the gradients by min(1, max_norm / (norm + 1e-6)) as they are read, with a float32
+        device tensor for the norm, which is no part of what is updated."""
         handle = self._handle(stream)
+        arg = None if clip is None else _clip_arg(clip, self.device)
+        was = self.hp.lr
         self.hp.step = int(step)
         if lr is not None:
             self.hp.lr = float(lr)
-        arg = None if clip is None else _clip_arg(clip, self.device)
-        self._call(lib().adamw_list_step_double, (ctypes.byref(self.hp), arg), stream, handle)
+        try:
+            self._call(lib().adamw_list_step_double, (ctypes.byref(self.hp), arg), stream, handle)
+        except Exception:
+            self.hp.lr = was  # a refused call changes nothing
+            raise
         if clip is not None:
             _keep_for(clip[0], stream, self.device)
 

@@ -204,6 +204,25 @@ def test_a_stream_of_another_device_is_refused(streams):
     assert not b.waits
 
 
+def test_a_refused_update_leaves_the_learning_rate(streams, monkeypatch):
+    rates, answers = [], [nm.MUON_OK, nm.MUON_EINVAL, nm.MUON_OK]
+
+    def step(lst, hp, clip, stream):
+        rates.append(hp._obj.lr)
+        return answers.pop(0)
+
+    lib = types.SimpleNamespace(adamw_list_step_double=step, muon_strerror=lambda c: b"", muon_last_error=lambda: b"")
+    monkeypatch.setattr(nm, "lib", lambda: lib)
+    a = streams(1)
+    adam = laid_out(a, nm.AdamWStep)
+    adam.hp = nm.adamw_hparams_double(0.5)
+    adam(1, lr=0.25, stream=a)
+    with pytest.raises(nm.MuonError):
+        adam(2, lr=float("nan"), stream=a)
+    adam(2, stream=a)
+    assert rates[0] == rates[2] == 0.25
+
+
 def test_stream_capture_arguments():
     out = ctypes.c_uint64(5)
     assert nm.lib().muon_stream_capture(None, None) == nm.MUON_EINVAL
