@@ -989,9 +989,14 @@ namespace {
 static_assert(sizeof(ListHandle) == sizeof(muon_grad_list) && sizeof(ListHandle) == sizeof(adamw_list),
               "a laid-out list holds one handle");
 
-// The identity of the capture that a stream takes part in, 0 for none.  A capture that was
-// broken off is refused.
+// The identity of the capture that a stream takes part in, 0 for none (always of the null
+// stream, which cannot be captured and may not be asked while another one is).  A capture that
+// was broken off is refused.
 int capture_of(hipStream_t s, uint64_t* id) {
+  if (!s) {
+    *id = 0;
+    return MUON_OK;
+  }
   hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
   unsigned long long x = 0;
   const hipError_t e = hipStreamGetCaptureInfo(s, &status, &x);

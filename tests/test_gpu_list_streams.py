@@ -208,3 +208,29 @@ def test_an_expanded_workspace_is_refused():
             nm.GradClip([g], workspace=bad)
         with pytest.raises(ValueError, match="contiguous"):
             nm.AdamWStep([g], [g.clone()], [g.clone()], [g.clone()], workspace=bad)
+
+
+@pytest.mark.parametrize("own", [False, True])  # eager norms on the default stream, or one of their own
+def test_eager_and_captured_norms_of_one_list(own):
+    """Eager norms before the capture, between captures and between replays."""
+    log("eager and captured norms")
+    views, _ = make(LISTS["long"], 107, std=1.0)
+    lst = nm.GradClip(views)
+    outs = [torch.zeros((), device=DEV) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    with torch.cuda.stream(torch.cuda.Stream() if own else torch.cuda.current_stream()):
+        for graph, out in zip(graphs, outs):
+            first = lst.norm()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                lst.norm(out=out)
+        for k in range(4):
+            graphs[k % 2].replay()
+            eager = lst.norm()
+            graphs[1 - k % 2].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], eager) and torch.equal(outs[1], eager)
+            assert norm_close(eager, grad_norm([to64(x) for x in views]))
+            for x in views:
+                x.mul_(0.5)
+        assert float(first) > 0.0

@@ -10,7 +10,6 @@ import pytest
 import torch
 
 import newton_schulz_02_amd as nm
-from tests.test_abi import _gpu_visible
 
 
 class Stream:
@@ -226,5 +225,4 @@ def test_a_refused_update_leaves_the_learning_rate(streams, monkeypatch):
 def test_stream_capture_arguments():
     out = ctypes.c_uint64(5)
     assert nm.lib().muon_stream_capture(None, None) == nm.MUON_EINVAL
-    if not _gpu_visible():
-        assert nm.lib().muon_stream_capture(None, ctypes.byref(out)) == nm.MUON_EHIP and out.value == 5
+    assert nm.lib().muon_stream_capture(None, ctypes.byref(out)) == nm.MUON_OK and out.value == 0  # the null stream
