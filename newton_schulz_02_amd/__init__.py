@@ -461,7 +461,8 @@ class MuonStep:
         _check(lib().muon_step_clipped(self.arr, self.count, ctypes.byref(self.hp), _clip_arg(clip, self.device),
                                        c_void_p(self.workspace.data_ptr()), self.workspace.numel(),
                                        _stream_handle(stream, self.device)))
-        _keep_for(clip[0], stream, self.device)
+        if stream is not None:
+            _keep_for(clip[0], stream, self.device)
 
     def check(self, stream=None) -> None:
         """Raise MuonError if the last step reported a failure (muon_workspace_check)."""
@@ -838,10 +839,9 @@ def _stream_of(stream, device):
 
 
 def _keep_for(tensor, stream, device) -> None:
-    """A call on a stream that the caller names reads or writes `tensor` when that stream gets
-    there: the allocator gives its memory to nobody before."""
-    if stream is not None:
-        tensor.record_stream(_stream_of(stream, device))
+    """After a call on a stream that the caller names: it reads or writes `tensor` when that
+    stream gets there, and the allocator gives its memory to nobody before."""
+    tensor.record_stream(_stream_of(stream, device))
 
 
 def _capture_of(handle: int) -> int:
@@ -866,6 +866,8 @@ class _List:
         self.ws_bytes = int(size.value)
         home = self._stream(stream)
         self._home = home.cuda_stream
+        # As bound functions: the names cost a short call's host as much as the calls.
+        self._current, self._current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         with torch.cuda.device(self.device), torch.cuda.stream(home):
             if workspace is None:
                 workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
@@ -893,11 +895,8 @@ class _List:
 
     def _handle(self, stream):
         """The handle of the stream of a call, which may use the list."""
-        import torch
-
         # The handle alone: a Stream object for the current stream costs as much as the launch.
-        handle = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else \
-            self._stream(stream).cuda_stream
+        handle = self._current(self.device.index) if stream is None else self._stream(stream).cuda_stream
         # Before the call allocates, or waits for anything: a wait for the layout would pull its
         # stream into the layout's capture, or break its own.
         if self._capture and _capture_of(handle) != self._capture:
@@ -906,13 +905,13 @@ class _List:
 
     def _call(self, fn, args, stream, handle):
         """fn(list, *args, stream) on the list's device."""
-        import torch
-
         if handle != self._home:
             self._elsewhere(self._stream(stream))
-        if torch.cuda.current_device() == self.device.index:
+        if self._current_device() == self.device.index:
             _check(fn(self._list, *args, handle))
         else:
+            import torch
+
             with torch.cuda.device(self.device):
                 _check(fn(self._list, *args, handle))
 
@@ -946,7 +945,7 @@ class GradClip(_List):
 
     def __init__(self, grads, *, device=None, workspace=None, stream=None):
         self.grads = list(grads)
-        self._norm_last, self._norm_streams = None, {}
+        self._norm_last, self._norm_streams = None, set()
         self._lay_out(grad_array(self.grads), len(self.grads), self.grads, device, workspace, stream)
 
     def _out(self, out, stream):
@@ -959,34 +958,32 @@ class GradClip(_List):
         with torch.cuda.stream(self._stream(stream)):
             return torch.empty((), dtype=torch.float32, device=self.device)
 
-    def _call_norm(self, fn, args, stream, handle):
-        if handle != self._norm_last:
-            self._in_turn(self._stream(stream))
-        self._call(fn, args, stream, handle)
-
-    def _in_turn(self, stream):
+    def _in_turn(self, handle):
         """Before a norm on another stream than the last one's: norms of a list count their
         workgroups in the list's workspace, so each comes after those before it.  A capture waits
         only for the norms inside it, and nothing outside waits for those."""
-        capture, still = _capture_of(stream.cuda_stream), {}
-        for handle, other in self._norm_streams.items():
-            if handle == stream.cuda_stream:
-                continue
-            inside = _capture_of(handle)
-            if inside == capture:
-                stream.wait_event(other.record_event())
-            if inside or capture:
-                still[handle] = other
-        still[stream.cuda_stream] = stream
-        self._norm_last, self._norm_streams = stream.cuda_stream, still
+        still = {handle}  # the streams that a later norm may have to wait for
+        if self._norm_streams:
+            capture = _capture_of(handle)
+            for other in self._norm_streams - still:
+                inside = _capture_of(other)
+                if inside == capture:
+                    self._stream(handle).wait_event(self._stream(other).record_event())
+                if inside or capture:
+                    still.add(other)
+        self._norm_last, self._norm_streams = handle, still
 
     def norm(self, kind="l2", *, out=None, stream=None):
         """The norm of all gradients, as a float32 device tensor (`out`, which is no part of a
         gradient, or a new one that belongs to the stream of the call)."""
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call_norm(lib().muon_grad_norm, (code, _norm_arg(out, self.device)), stream, handle)
-        _keep_for(out, stream, self.device)
+        arg = _norm_arg(out, self.device)
+        if handle != self._norm_last:
+            self._in_turn(handle)
+        self._call(lib().muon_grad_norm, (code, arg), stream, handle)
+        if stream is not None:
+            _keep_for(out, stream, self.device)
         return out
 
     def clip(self, norm, max_norm, *, stream=None) -> None:
@@ -994,15 +991,19 @@ class GradClip(_List):
         device tensor, for example one that was reduced over ranks, and no part of a gradient."""
         handle = self._handle(stream)
         self._call(lib().muon_grad_clip, (_clip_arg((norm, max_norm), self.device),), stream, handle)
-        _keep_for(norm, stream, self.device)
+        if stream is not None:
+            _keep_for(norm, stream, self.device)
 
     def clip_norm(self, max_norm, kind="l2", *, out=None, stream=None):
         """norm(), then clip() by it; returns the norm from before."""
         code, handle = _norm_kind(kind), self._handle(stream)
         out = self._out(out, stream)
-        self._call_norm(lib().muon_grad_clip_norm, (code, c_float(max_norm), _norm_arg(out, self.device)), stream,
-                        handle)
-        _keep_for(out, stream, self.device)
+        arg = _norm_arg(out, self.device)
+        if handle != self._norm_last:
+            self._in_turn(handle)
+        self._call(lib().muon_grad_clip_norm, (code, c_float(max_norm), arg), stream, handle)
+        if stream is not None:
+            _keep_for(out, stream, self.device)
         return out
 
 
@@ -1030,16 +1031,16 @@ class AdamWStep(_List):
         device tensor for the norm, which is no part of what is updated."""
         handle = self._handle(stream)
         arg = None if clip is None else _clip_arg(clip, self.device)
-        was = self.hp.lr
         self.hp.step = int(step)
         if lr is not None:
-            self.hp.lr = float(lr)
+            was, self.hp.lr = self.hp.lr, float(lr)
         try:
             self._call(lib().adamw_list_step_double, (ctypes.byref(self.hp), arg), stream, handle)
         except Exception:
-            self.hp.lr = was  # a refused call changes nothing
+            if lr is not None:
+                self.hp.lr = was  # a refused call changes nothing
             raise
-        if clip is not None:
+        if clip is not None and stream is not None:
             _keep_for(clip[0], stream, self.device)
 
 

@@ -31,7 +31,8 @@ def laid_out(home, cls=nm.GradClip):
     lst.device, lst.count = torch.device("cuda", 0), 0
     lst._home, lst._capture, lst._laid_out = home.cuda_stream, home.capture, home.record_event()
     lst._ordered = {lst._home}
-    lst._norm_last, lst._norm_streams = None, {}
+    lst._current_device = lambda: 0
+    lst._norm_last, lst._norm_streams = None, set()
     lst.workspace = types.SimpleNamespace(record_stream=lambda s: None)
     lst.list = lst._list = None
     return lst
@@ -47,7 +48,7 @@ def streams(monkeypatch):
         return known[handle]
 
     monkeypatch.setattr(nm, "_capture_of", lambda handle: known[handle].capture)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: known[handle])
     return make
 
 
@@ -97,7 +98,9 @@ def test_an_eager_list_waits_once_for_its_layout(streams):
 
 def norm(lst, stream):
     fn, seen = calls()
-    lst._call_norm(fn, (), stream, lst._handle(stream))
+    with pytest.MonkeyPatch.context() as patch:
+        patch.setattr(nm, "lib", lambda: types.SimpleNamespace(muon_grad_norm=fn))
+        lst.norm(out=Value(), stream=stream)
     assert len(seen) == 1
 
 
