@@ -18,7 +18,6 @@
  *             w <- w - lr ((m / (1-b1^t)) / (sqrt(v / (1-b2^t)) + eps) + weight_decay decay w);
  *             param <- w, rounded to param's type.
  *   muon_step_clipped runs muon_step with M <- beta M + c G.
- * muon_step_clipped runs muon_step with M <- beta M + c G.
  * The norm is a float in device memory, so clipping needs no transfer to the host.  Where
  * several ranks own parts of the gradients, each takes its part's norm, the caller reduces
  * them (sum of squares, or maximum), and every rank clips by the reduced value.

@@ -939,7 +939,8 @@ class GradClip(_List):
     a named stream may be dropped after the call; the gradients are kept by this object alone.
     Replays of graphs are not calls:
     graphs that hold norms of one list are replayed one after another (and after eager norms of
-    it), or each has a list of its own."""
+    it), or each has a list of its own.  A graph keeps nothing alive: one that was captured with
+    this needs it, and its tensors, as long as it is replayed."""
 
     _kind = "muon_grad_list"
 
@@ -1011,8 +1012,9 @@ class AdamWStep(_List):
     """AdamW over fixed lists of device tensors, laid out once (see adamw_array for the lists).
 
     Each call enqueues one ``adamw_list_step`` on the current (or given) stream.  As with
-    GradClip, the tensors stay where they are and the layout goes to `stream`.  Every call updates
-    the tensors, so the caller orders calls on several streams."""
+    GradClip, the tensors stay where they are, the layout goes to `stream`, and a graph needs this
+    as long as it is replayed (each replay with the step and rates that were captured).  Every
+    call updates the tensors, so the caller orders calls on several streams."""
 
     _kind = "adamw_list"
 

@@ -4,13 +4,15 @@
 // A list is a table of tensors cut into chunks (list_plan.h); a workgroup takes chunks
 // blockIdx.x, blockIdx.x + gridDim.x, ... and finds each one's tensor in the list's map.  All
 // three kernels are HBM-bound:
-//   norm   reads every gradient once: one 4096-hidden layer in bf16 (405 MB) in 61.5 us, 6.6
-//          TB/s; 512 small fp32 matrices (1.4 GB) in 200 us, 7.0 TB/s.  The squares' 64-bit
-//          sums hide under the loads: the inf norm, an integer maximum, is 1 % faster.
-//   clip   reads and writes them: 126 us, 6.4 TB/s; 450 us, 6.3 TB/s.
+//   norm   reads every gradient once: one 4096-hidden layer in bf16 (405 MB) in 64 us, 6.3
+//          TB/s; 512 small fp32 matrices (1.4 GB) in 197 us, 7.2 TB/s.  The squares' 64-bit
+//          sums hide under the loads: the inf norm, an integer maximum, takes as long.
+//   clip   reads and writes them: 128 us, 6.3 TB/s; 476 us, 5.9 TB/s.
 //   AdamW  reads and writes its state once: two 32000 x 4096 embeddings with masters and bf16
-//          gradients (7.3 GB) in 1.17 ms, 6.3 TB/s.
-// (A copy by the runtime's own kernel moves 4.9 TB/s on the same card.)
+//          gradients (7.3 GB) in 1.19 ms, 6.2 TB/s.
+// (Medians of each kernel alone, launched in turn over three sets of tensors.  Times beside a
+// choice below are of calls queued one behind the other, a few per cent shorter, and of one run
+// each.  A copy by the runtime's own kernel moves 4.9 TB/s on the same card.)
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -45,9 +47,11 @@ __global__ __launch_bounds__(256) void k_list_map(const Rec* recs, int count, ui
   }
 }
 
-// 16 bytes of S elements, read and written with one access wherever they lie: a tensor may
-// start at any element (gfx950 takes unaligned 16-byte accesses; the address space keeps them
-// global, since FLAT ones would also hold up the LDS waits).  Non-temporal, as every list
+// 16 bytes of S elements, read and written with one access.  Chunks start on line boundaries, so
+// the accesses of norm and clip are aligned wherever a tensor starts; the types say no more than
+// an element's alignment (which gfx950 takes too, and which AdamW's load4 and store4 need, whose
+// buffers lie differently).  The address space keeps them global, since FLAT ones would also
+// hold up the LDS waits.  Non-temporal, as every list
 // access below: nothing is used twice by one kernel.  That is worth a tenth: the norm of a bf16
 // layer takes 63.6 us with it and 70.4 us without, its clipping 126 and 145 us.
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -259,8 +263,8 @@ __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
   const float coef = clip_coef(a.clip);
   if (coef == 1.0f) return;
   Scale scale{coef};
-  // By half chunks (512 small fp32 matrices, 1.4 GB: 450 us by 16 KiB, 475 by 32 KiB and by
-  // 8 KiB), and backwards, since what the norm read last may still be in the memory-side cache
+  // By half chunks (512 small fp32 matrices, 1.4 GB, a workgroup for each: 450 us by 16 KiB, 475
+  // by 32 KiB and by 8 KiB; 468 by 16 KiB in the grid below), and backwards, since what the norm read last may still be in the memory-side cache
   // (1 % of a layer's clipping).
   for (uint32_t b = blockIdx.x; b < 2 * a.chunks; b += gridDim.x) {
     const uint32_t h = 2 * a.chunks - 1 - b;

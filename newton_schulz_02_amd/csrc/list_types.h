@@ -30,8 +30,11 @@ constexpr int kTickets = 8;            // groups in which a norm's workgroups co
 constexpr int64_t kListTickets = 256;  // a list's workspace: status word, counts, entries
 constexpr int64_t kListHead = kListTickets + (kTickets + 1) * kLine;
 constexpr int64_t kGradChunk = 32768;  // bytes of one chunk of a gradient list
-// Elements of one chunk of an AdamW list: 2048 against 1024, us: bf16 param and gradient
-// 469 / 498, fp32 305 / 300, bf16 with master 1231 / 1201; 4096 is slower for all.
+// Elements of one chunk of an AdamW list: 2048 in runs of 16 per XCD against 1024 in runs of 32
+// (which are better than of 16), us: bf16 param and gradient 461 / 489, with 37 x 1031 elements a
+// tensor 139 / 150; bf16 with master 1168 / 1186, with fp32 gradients 321 / 312; bf16 with fp32
+// gradients 262 / 263; fp32 305 / 290, with bf16 gradients 283 / 271; a ragged mixed list and
+// short ones the same.  One size for all: 2048 gains 6 % where it gains, and loses 5 % on fp32.
 constexpr int64_t kAdamChunk = 2048;
 // Most workgroups (and partial results) of a norm: a few long ones, each 32 KiB of loads ahead.
 // us of a 4096-hidden layer in bf16 / of 512 small fp32 matrices: 512 workgroups 61.5 / 200,
