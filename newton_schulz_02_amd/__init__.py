@@ -935,7 +935,8 @@ class GradClip(_List):
     after gradients were replaced by other tensors, make a new one.  The layout is enqueued on
     `stream` (default: the current one) at construction; calls on other streams wait for it.
     Inside a graph capture it is recorded, and only calls on streams of that capture can use it.
-    Norms on several streams run in the order of the calls.  A norm that is passed or written on
+    Norms on several streams run in the order of the calls; a stream whose handle is passed lives
+    as long as this is used.  A norm that is passed or written on
     a named stream may be dropped after the call; the gradients are kept by this object alone.
     Replays of graphs are not calls:
     graphs that hold norms of one list are replayed one after another (and after eager norms of
