@@ -936,12 +936,13 @@ class GradClip(_List):
     `stream` (default: the current one) at construction; calls on other streams wait for it.
     Inside a graph capture it is recorded, and only calls on streams of that capture can use it.
     Norms on several streams run in the order of the calls; a stream whose handle is passed lives
-    as long as this is used.  A norm that is passed or written on
-    a named stream may be dropped after the call; the gradients are kept by this object alone.
-    Replays of graphs are not calls:
-    graphs that hold norms of one list are replayed one after another (and after eager norms of
-    it), or each has a list of its own.  A graph keeps nothing alive: one that was captured with
-    this needs it, and its tensors, as long as it is replayed."""
+    as long as this is used.  A norm that is passed or written on a named stream may be dropped
+    after the call; gradients may not, before the stream has passed it.
+
+    Replays of graphs are not calls: graphs that hold norms of one list are replayed one after
+    another (and after eager norms of it), or each has a list of its own.  A graph keeps nothing
+    alive: one that was captured with this needs it, and its tensors, as long as it is
+    replayed."""
 
     _kind = "muon_grad_list"
 

@@ -264,8 +264,8 @@ __global__ __launch_bounds__(256) void k_grad_clip(GradArgs a) {
   if (coef == 1.0f) return;
   Scale scale{coef};
   // By half chunks (512 small fp32 matrices, 1.4 GB, a workgroup for each: 450 us by 16 KiB, 475
-  // by 32 KiB and by 8 KiB; 468 by 16 KiB in the grid below), and backwards, since what the norm read last may still be in the memory-side cache
-  // (1 % of a layer's clipping).
+  // by 32 KiB and by 8 KiB; 468 by 16 KiB in the grid below), and backwards, since what the norm
+  // read last may still be in the memory-side cache (1 % of a layer's clipping).
   for (uint32_t b = blockIdx.x; b < 2 * a.chunks; b += gridDim.x) {
     const uint32_t h = 2 * a.chunks - 1 - b;
     const uint32_t c = h >> 1;
