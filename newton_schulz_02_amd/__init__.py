@@ -8,9 +8,11 @@ Entry points mirror ``include/muon.h``: :func:`workspace_size`, :func:`muon_step
 :func:`adamw_step`, :func:`step_cost`, :func:`plan_describe`, :func:`profile_begin`,
 :func:`profile_end`, :func:`strerror`, :func:`last_error`, :func:`version`,
 :func:`shutdown`; ``include/shampoo.h``: :func:`shampoo_workspace_size`,
-:func:`shampoo_step` (:class:`ShampooStep`), :func:`shampoo_plan_describe`; and
+:func:`shampoo_step` (:class:`ShampooStep`), :func:`shampoo_plan_describe`;
 ``include/muon_grad.h``: :func:`grad_norm`, :func:`grad_clip`, :func:`clip_grad_norm`
-(:class:`GradClip`), :func:`adamw_list_step` (:class:`AdamWStep`).
+(:class:`GradClip`), :func:`adamw_list_step` (:class:`AdamWStep`); and
+``include/muon_linear.h``: :func:`quantize` (:class:`Codes`), :func:`dequantize`,
+:func:`int8_matmul`, :func:`int8_linear`, :func:`weight_grad`.
 """
 
 from __future__ import annotations
@@ -106,7 +108,19 @@ class muon_clip(ctypes.Structure):
     _fields_ = [("norm", c_void_p), ("max_norm", c_float), ("reserved", c_int32)]
 
 
+class muon_view(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("rows", c_int64), ("cols", c_int64), ("ld", c_int64), ("dtype", c_int32),
+                ("reserved", c_int32)]
+
+
+class muon_codes(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("scale", c_void_p), ("rows", c_int64), ("cols", c_int64), ("block", c_int32),
+                ("reserved", c_int32)]
+
+
 _MATP = POINTER(muon_matrix)
+_VIEWP = POINTER(muon_view)
+_CODESP = POINTER(muon_codes)
 _HPP = POINTER(muon_hparams)
 _SMATP = POINTER(shampoo_matrix)
 _SHPP = POINTER(shampoo_hparams)
@@ -156,6 +170,15 @@ _SIGNATURES = {
     "adamw_list_init": (c_int, [POINTER(adamw_tensor), c_int32, c_void_p, c_size_t, c_void_p, POINTER(adamw_list)]),
     "adamw_list_step": (c_int, [POINTER(adamw_list), POINTER(adamw_hparams), POINTER(muon_clip), c_void_p]),
     "adamw_list_step_double": (c_int, [POINTER(adamw_list), POINTER(adamw_hparams_double), POINTER(muon_clip), c_void_p]),
+    "muon_quantize_size": (c_int, [_VIEWP, c_int32, POINTER(c_size_t)]),
+    "muon_quantize": (c_int, [_VIEWP, c_int32, _CODESP, c_void_p, c_size_t, c_void_p]),
+    "muon_dequantize": (c_int, [_CODESP, _VIEWP, c_void_p]),
+    "muon_int8_matmul_size": (c_int, [_CODESP, _CODESP, POINTER(c_size_t)]),
+    "muon_int8_matmul": (c_int, [_CODESP, _CODESP, _VIEWP, c_void_p, c_size_t, c_void_p]),
+    "muon_int8_linear_size": (c_int, [_VIEWP, _CODESP, POINTER(c_size_t)]),
+    "muon_int8_linear": (c_int, [_VIEWP, _CODESP, _VIEWP, c_void_p, c_size_t, c_void_p]),
+    "muon_weight_grad_size": (c_int, [_VIEWP, _CODESP, POINTER(c_size_t)]),
+    "muon_weight_grad": (c_int, [_VIEWP, _CODESP, _VIEWP, c_int32, c_void_p, c_size_t, c_void_p]),
 }
 
 _lib = None
@@ -1067,3 +1090,205 @@ def clip_grad_norm(grads, max_norm, kind="l2", *, device=None, stream=None):
 def adamw_list_step(params, grads, ms, vs, *, step=1, clip=None, stream=None, **kw) -> None:
     """One AdamW update of lists of tensors (see AdamWStep), laid out for this call."""
     AdamWStep(params, grads, ms, vs, stream=stream, **kw)(step, clip=clip, stream=stream)
+
+
+# --- 8-bit operators of linear layers (include/muon_linear.h) ----------------------------
+
+CODE_BLOCK = 128  #: columns of a block scale; rows of codes are padded to a multiple of it
+
+
+class Codes:
+    """8-bit codes of a rows x cols matrix with their scales (see :func:`quantize`).
+
+    q: int8, rows x the padded row length (zeros behind the cols codes of a row); scale: float32,
+    one per row, or for codes by block one per row and 128 columns.  They are fixed at
+    construction; their values may change."""
+
+    def __init__(self, q, scale, cols, *, block=False):
+        import torch
+
+        rows, cols = q.shape[0], int(cols)
+        groups = -(-cols // CODE_BLOCK) if block else 1
+        if q.dtype != torch.int8 or not q.is_contiguous() or tuple(q.shape) != (rows, -(-cols // CODE_BLOCK) * CODE_BLOCK):
+            raise ValueError(f"q must be contiguous int8 of rows x {-(-cols // CODE_BLOCK) * CODE_BLOCK}")
+        if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() != rows * groups:
+            raise ValueError(f"scale must be contiguous float32 of {rows} x {groups} values")
+        _linear_device({"q": q, "scale": scale})
+        self.q, self.scale, self.block, self.shape = q, scale, bool(block), (rows, cols)
+        self.device = q.device
+        self._arg = ctypes.byref(muon_codes(q.data_ptr(), scale.data_ptr(), rows, cols, CODE_BLOCK if block else 0, 0))
+
+    @classmethod
+    def empty(cls, rows, cols, *, block=False, device=None):
+        """Memory for the codes of a rows x cols matrix, its contents undefined."""
+        import torch
+
+        device = torch.device("cuda" if device is None else device)
+        q = torch.empty((rows, -(-cols // CODE_BLOCK) * CODE_BLOCK), dtype=torch.int8, device=device)
+        shape = (rows, -(-cols // CODE_BLOCK)) if block else (rows,)
+        return cls(q, torch.empty(shape, dtype=torch.float32, device=device), cols, block=block)
+
+    def dequantize(self, dtype=None, *, out=None, stream=None):
+        """The values that the codes stand for (see :func:`dequantize`)."""
+        return dequantize(self, dtype, out=out, stream=stream)
+
+
+def _linear_device(tensors):
+    """The one GPU that named tensors (or Codes) are on."""
+    device = None
+    for name, t in tensors.items():
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a GPU, not on {t.device}")
+        if device is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, other operands are on {device}")
+        device = t.device
+    return device
+
+
+def _view_arg(name, t):
+    """A 2D tensor whose rows are contiguous (they may lie apart) as a muon_view."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2D")
+    (rows, cols), (ld, inner) = t.shape, t.stride()
+    if cols > 1 and inner != 1 or rows > 1 and ld < cols:
+        raise ValueError(f"{name}: rows must be contiguous and not overlap (shape {tuple(t.shape)}, strides {t.stride()})")
+    return ctypes.byref(muon_view(t.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_code(t), 0))
+
+
+def _linear_out(out, shape, dtype, default, device, stream):
+    """A call's result: `out`, which has to fit, or a new tensor that belongs to the call's stream."""
+    import torch
+
+    if out is None:
+        with _on_stream(stream, device):
+            return torch.empty(shape, dtype=default if dtype is None else dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {tuple(shape)}" + ("" if dtype is None else f" of {dtype}"))
+    return out
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return None
+
+
+_NOTHING = _Nothing()
+
+
+def _on_stream(stream, device):
+    """Where a call allocates: on the stream that it names, else on the current one."""
+    import torch
+
+    return _NOTHING if stream is None else torch.cuda.stream(_linear_stream(stream, device))
+
+
+def _linear_stream(stream, device):
+    stream = _stream_of(stream, device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+    return stream
+
+
+def _linear_call(size_fn, size_args, fn, args, device, stream, tensors) -> None:
+    """fn(*args, workspace, its bytes, stream) on the operands' device, with a workspace of the size
+    that size_fn names (size_fn None: fn takes no workspace); `tensors` are what the call uses."""
+    import torch
+
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _linear_call(size_fn, size_args, fn, args, device, stream, tensors)
+    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
+        _linear_stream(stream, device).cuda_stream
+    if size_fn is None:
+        _check(fn(*args, handle))
+    else:
+        need = c_size_t(0)
+        _check(size_fn(*size_args, ctypes.byref(need)))
+        if need.value:
+            # On the call's stream: its block goes to nobody else before that stream has passed.
+            with _on_stream(stream, device):
+                workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+            _check(fn(*args, workspace.data_ptr(), need.value, handle))
+        else:
+            _check(fn(*args, None, 0, handle))
+    if stream is not None:
+        for t in tensors:
+            for x in (t.q, t.scale) if isinstance(t, Codes) else (t,):
+                _keep_for(x, stream, device)
+
+
+def quantize(x, *, block=False, transpose=False, out=None, stream=None) -> Codes:
+    """8-bit codes of a 2D tensor (bfloat16 or float32; rows may lie apart).
+
+    By row (the operands of int8_matmul): scale = max|row| / 127, code = the integer nearest to
+    127 x / max|row|.  With block=True (a checkpoint, for weight_grad) by 128 columns of a row,
+    with the smallest power of two that fits them as the scale.  transpose=True gives the codes
+    of x's columns, as rows (codes by row only): a weight's for the input gradient.  `out`: Codes
+    to write to.  A row or block with a NaN or an infinity stands for NaN."""
+    device = _linear_device({"x": x} if out is None else {"x": x, "out": out})
+    xv = _view_arg("x", x)
+    shape = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
+    if block and transpose:
+        raise ValueError("codes of columns are by row only (block=False)")
+    if out is None:
+        with _on_stream(stream, device):
+            out = Codes.empty(*shape, block=block, device=device)
+    elif out.shape != shape or out.block != bool(block):
+        raise ValueError(f"out must be Codes of {shape} with block={bool(block)}")
+    t = 1 if transpose else 0
+    _linear_call(lib().muon_quantize_size if t else None, (xv, t), lib().muon_quantize,
+                 (xv, t, out._arg) if t else (xv, t, out._arg, None, 0), device, stream, (x, out))
+    return out
+
+
+def dequantize(codes, dtype=None, *, out=None, stream=None):
+    """The values that codes stand for, code * scale, in bfloat16 (default) or float32."""
+    import torch
+
+    device = _linear_device({"codes": codes} if out is None else {"codes": codes, "out": out})
+    out = _linear_out(out, codes.shape, dtype, torch.bfloat16, device, stream)
+    _linear_call(None, (), lib().muon_dequantize, (codes._arg, _view_arg("out", out)), device, stream, (codes, out))
+    return out
+
+
+def int8_matmul(a, b, dtype=None, *, out=None, stream=None):
+    """a b^T of two Codes by row (tokens x inputs, channels x inputs): sums of 8-bit products in
+    32-bit integers, times the scales of token and channel, in bfloat16 (default) or float32."""
+    import torch
+
+    device = _linear_device({"a": a, "b": b} if out is None else {"a": a, "b": b, "out": out})
+    out = _linear_out(out, (a.shape[0], b.shape[0]), dtype, torch.bfloat16, device, stream)
+    args = (a._arg, b._arg)
+    _linear_call(lib().muon_int8_matmul_size, args, lib().muon_int8_matmul, (*args, _view_arg("out", out)), device,
+                 stream, (a, b, out))
+    return out
+
+
+def int8_linear(x, w, dtype=None, *, out=None, stream=None):
+    """int8_matmul(quantize(x), w), bit for bit, in x's dtype by default; for a few rows of x in one
+    launch."""
+    device = _linear_device({"x": x, "w": w} if out is None else {"x": x, "w": w, "out": out})
+    args = (_view_arg("x", x), w._arg)
+    out = _linear_out(out, (x.shape[0], w.shape[0]), dtype, x.dtype, device, stream)
+    _linear_call(lib().muon_int8_linear_size, args, lib().muon_int8_linear, (*args, _view_arg("out", out)), device,
+                 stream, (x, w, out))
+    return out
+
+
+def weight_grad(dy, x, dtype=None, *, out=None, accumulate=False, stream=None):
+    """dy^T x (outputs x inputs) from dy (tokens x outputs, bfloat16 or float32) and the checkpoint
+    of x, Codes by block: the gradient of W in y = x W^T, in float32 (default) or bfloat16.  With
+    accumulate=True it is added to `out`, the gradient so far."""
+    import torch
+
+    device = _linear_device({"dy": dy, "x": x} if out is None else {"dy": dy, "x": x, "out": out})
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out, the gradient to add to")
+    args = (_view_arg("dy", dy), x._arg)
+    out = _linear_out(out, (dy.shape[1], x.shape[1]), dtype, torch.float32, device, stream)
+    _linear_call(lib().muon_weight_grad_size, args, lib().muon_weight_grad,
+                 (*args, _view_arg("out", out), 1 if accumulate else 0), device, stream, (dy, x, out))
+    return out

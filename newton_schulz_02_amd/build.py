@@ -24,27 +24,30 @@ BUILD = PKG / "_build"
 LIB = PKG / "libmuon.so"
 ARCH = "gfx950"
 
-SOURCES = ["planner.cpp", "shampoo_plan.cpp", "list_plan.cpp", "muon_api.cpp", "owner.cpp", "kernels_elementwise.hip",
-           "kernels_list.hip", "kernels_gemm.hip", "kernels_gemm_wide.hip", "noalloc.hip"]
+SOURCES = ["planner.cpp", "shampoo_plan.cpp", "list_plan.cpp", "linear_plan.cpp", "muon_api.cpp", "owner.cpp",
+           "kernels_elementwise.hip", "kernels_list.hip", "kernels_quant.hip", "kernels_int8.hip", "kernels_wgrad.hip",
+           "kernels_gemm.hip", "kernels_gemm_wide.hip", "noalloc.hip"]
 # Sources compiled a second time with extra defines: (source, object stem, flags).
 VARIANTS = [("kernels_gemm.hip", "kernels_gemm_deep", ["-DMUON_GEMM_DEEP=1"]),
             ("kernels_gemm.hip", "kernels_gemm_small", ["-DMUON_GEMM_SMALL=1"])]
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
 
-# Sources of the list operators, which no tuned launch runs.
+# Sources of the list operators and of the 8-bit linear operators, which no tuned launch runs.
 LIST_SOURCES = {"kernels_list.hip", "list_math.h", "list_plan.h", "list_types.h"}
+LINEAR_SOURCES = {"kernels_quant.hip", "kernels_int8.hip", "kernels_wgrad.hip", "linear_math.h", "linear_plan.h",
+                  "linear_types.h", "tile_store.h"}
 
 
 def kernel_hash() -> str:
-    """Hash of the device sources (every .hip and .h file under csrc but the list operators'),
-    16 hex digits.
+    """Hash of the device sources (every .hip and .h file under csrc but the list and the
+    8-bit linear operators'), 16 hex digits.
 
     Compiled into the library (muon_kernel_hash); a tuning table records the hash of the
     kernels it was measured on, and a library built from other sources refuses it."""
     h = hashlib.sha256()
     for p in sorted(CSRC.glob("*.hip")) + sorted(CSRC.glob("*.h")):
-        if p.name in LIST_SOURCES:
+        if p.name in LIST_SOURCES or p.name in LINEAR_SOURCES:
             continue
         h.update(p.name.encode())
         h.update(p.read_bytes())

@@ -1,0 +1,286 @@
+// Quantising to 8-bit codes and reading them back, for gfx950 (muon_linear.h).  All of it is
+// HBM-bound: a value is read once (twice where the columns' maxima come first), its code
+// written once.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "linear_math.h"
+#include "linear_types.h"
+
+using namespace muon;
+
+namespace {
+
+// Maximum over the LANES (a power of two up to 64) neighbouring lanes of each group.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+#pragma unroll
+  for (int d = 1; d < LANES; d *= 2) v = max(v, uint32_t(__shfl_xor(int(v), d)));
+  return v;
+}
+
+// Codes of rows.  L lanes take a row together: a wave (short rows, four to a workgroup), or a
+// workgroup of 256 or 1024 lanes.  The first kKeep chunks of 8 values of each lane stay in
+// registers between the maximum and the codes; longer rows are read again (they come from L2).
+constexpr int kKeep = 4;
+template <typename T, int L>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
+  constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L;
+  __shared__ uint32_t tops[2][L > 64 ? L / 64 : 1];
+  const int lane = threadIdx.x % L;
+  const int chunks = a.pitch / 8;
+  int turn = 0;
+  for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / L; row < a.rows; row += int64_t(gridDim.x) * kRows) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ld;
+    Eight<T> v[kKeep];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) v[i].load(x, (lane + i * L) * 8, a.cols);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) top = max(top, v[i].top());
+    for (int c = lane + kKeep * L; c < chunks; c += L) {
+      Eight<T> w;
+      w.load(x, c * 8, a.cols);
+      top = max(top, w.top());
+    }
+    top = lanes_max<64>(top);
+    if constexpr (L > 64) {
+      // The two halves of `tops` take turns, so one barrier a row is enough.
+      if ((threadIdx.x & 63) == 0) tops[turn & 1][threadIdx.x / 64] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < L / 64; ++w) top = max(top, tops[turn & 1][w]);
+      ++turn;
+    }
+    const RowCoder code(top);
+    if (lane == 0) a.scale[row] = code.scale();
+    int8_t* q = a.q + row * a.pitch;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (lane + i * L < chunks) store_codes(q + (lane + i * L) * 8, code.eight(v[i]));
+    for (int c = lane + kKeep * L; c < chunks; c += L) {
+      Eight<T> w;
+      w.load(x, c * 8, a.cols);
+      store_codes(q + c * 8, code.eight(w));
+    }
+  }
+}
+
+// Codes of blocks: 16 lanes take a block of 128 values, so a wave reads 1 KB (bf16) at once.  A
+// workgroup takes kUnits x 256 consecutive chunks of 8 values, all in flight together.
+constexpr int kUnits = 4;
+template <typename T>
+__global__ __launch_bounds__(256) void k_quant_blocks(QuantArgs a, int64_t total) {
+  const int chunks = a.pitch / 8;
+  for (int64_t base = int64_t(blockIdx.x) * (kUnits * 256); base < total; base += int64_t(gridDim.x) * (kUnits * 256)) {
+    const int64_t row0 = base / chunks;
+    const int c0 = int(base - row0 * chunks);
+    Eight<T> v[kUnits];
+    int64_t row[kUnits];
+    int c[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = c0 + u * 256 + int(threadIdx.x);
+      row[u] = row0 + at / chunks;
+      c[u] = at % chunks;
+      v[u].clear();
+      if (row[u] < a.rows) v[u].load(static_cast<const T*>(a.x) + row[u] * a.ld, c[u] * 8, a.cols);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t top = lanes_max<16>(v[u].top());
+      if (row[u] >= a.rows) continue;
+      const BlockCoder code(top);
+      store_codes(a.q + row[u] * a.pitch + c[u] * 8, code.eight(v[u]));
+      const int group = c[u] / 16;
+      if (c[u] % 16 == 0 && group * kCodeBlock < a.cols)
+        a.scale[row[u] * ((a.cols + kCodeBlock - 1) / kCodeBlock) + group] = code.scale();
+    }
+  }
+}
+
+// Codes of columns, first launch: parts[s][c] <- the maximum of column c over row strip s of x.
+// A workgroup takes 256 columns (32 lanes of 8) and 8 rows at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void k_quant_cols_max(QuantArgs a) {
+  __shared__ uint32_t tops[8][256 + 8];
+  const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
+  const int cols = int(a.rows), rows = a.cols;  // of x
+  const int strip = (rows + a.part_rows - 1) / a.part_rows;
+  const int lo = int(blockIdx.y) * strip, hi = min(rows, lo + strip);
+  const int col = int(blockIdx.x) * 256 + lane * 8;
+  uint32_t top[8] = {};
+  for (int r = lo + sub; r < hi; r += 32) {
+    Eight<T> v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u].clear();
+      if (r + 8 * u < hi) v[u].load(static_cast<const T*>(a.x) + int64_t(r + 8 * u) * a.ld, col, cols);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top[e] = max(top[e], v[u].bits(e));
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) tops[sub][lane * 8 + e] = top[e];
+  __syncthreads();
+  const int c = threadIdx.x;
+  uint32_t t = 0;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) t = max(t, tops[s][c]);
+  if (blockIdx.x * 256 + c < cols) a.parts[int64_t(blockIdx.y) * cols + blockIdx.x * 256 + c] = __uint_as_float(t);
+}
+
+// Second launch: 128 columns of x by 128 rows to 128 rows of codes by 128, through LDS.  A lane
+// has 8 columns and, at a time, 4 consecutive rows: four codes of one column go to LDS as one
+// word.  Rows of 33 words: the words of neighbouring lanes lie 8 banks apart.
+template <typename T>
+__global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
+  __shared__ uint32_t tile[128 * 33];
+  __shared__ uint32_t tops[2][128];
+  const int cols = int(a.rows), rows = a.cols;  // of x
+  const int across = (cols + 127) / 128;
+  const int c0 = int(blockIdx.x) % across * 128, r0 = int(blockIdx.x) / across * 128;
+  {
+    const int c = threadIdx.x & 127, half = threadIdx.x >> 7;
+    uint32_t t = 0;
+    if (c0 + c < cols)
+      for (int s = half; s < a.part_rows; s += 2) t = max(t, __float_as_uint(a.parts[int64_t(s) * cols + c0 + c]));
+    tops[half][c] = t;
+  }
+  const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
+  Eight<T> v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int r = r0 + (u >> 2) * 64 + sub * 4 + (u & 3);
+    v[u].clear();
+    if (r < rows) v[u].load(static_cast<const T*>(a.x) + int64_t(r) * a.ld, c0 + lane * 8, cols);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const RowCoder code(max(tops[0][lane * 8 + e], tops[1][lane * 8 + e]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w |= uint32_t(code.one(v[4 * h + j].get(e)) & 255) << (8 * j);
+      tile[(lane * 8 + e) * 33 + h * 16 + sub] = w;
+    }
+  }
+  __syncthreads();
+  if (r0 == 0 && threadIdx.x < 128 && c0 + int(threadIdx.x) < cols)
+    a.scale[c0 + threadIdx.x] = RowCoder(max(tops[0][threadIdx.x], tops[1][threadIdx.x])).scale();
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = u * 32 + int(threadIdx.x) / 8, part = int(threadIdx.x) & 7;
+    if (c0 + c >= cols) continue;
+    const uint32_t* w = tile + c * 33 + part * 4;
+    *reinterpret_cast<uint4*>(a.q + int64_t(c0 + c) * a.pitch + r0 + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Values of codes: a lane takes 8 of one row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_dequant(DequantArgs a, int64_t total) {
+  const int chunks = (a.cols + 7) / 8;
+  for (int64_t base = int64_t(blockIdx.x) * (kUnits * 256); base < total; base += int64_t(gridDim.x) * (kUnits * 256)) {
+    const int64_t row0 = base / chunks;
+    const int c0 = int(base - row0 * chunks);
+    uint2 q[kUnits];
+    float s[kUnits];
+    int64_t row[kUnits];
+    int c[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = c0 + u * 256 + int(threadIdx.x);
+      row[u] = row0 + at / chunks;
+      c[u] = at % chunks;
+      if (row[u] < a.rows) {
+        q[u] = *reinterpret_cast<const uint2*>(a.q + row[u] * a.pitch + c[u] * 8);
+        s[u] = a.block ? a.scale[row[u] * ((a.cols + kCodeBlock - 1) / kCodeBlock) + c[u] / 16] : a.scale[row[u]];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      if (row[u] < a.rows) {
+        float f[8];
+        decode8(q[u], s[u], f);
+        Eight<T>::store(static_cast<T*>(a.out) + row[u] * a.ld, c[u] * 8, a.cols, f);
+      }
+  }
+}
+
+// Rows of bf16 to rows of ldd elements (a multiple of 8), zeros behind their end.
+__global__ __launch_bounds__(256) void k_pack_rows(const uint16_t* src, int64_t ld, uint16_t* dst, int64_t ldd,
+                                                   int64_t rows, int32_t cols) {
+  const int chunks = int(ldd / 8);
+  const int64_t total = rows * chunks;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / chunks;
+    const int c = int(i - row * chunks);
+    Eight<uint16_t> v;
+    v.load(src + row * ld, c * 8, cols);
+    *reinterpret_cast<uint4*>(dst + row * ldd + c * 8) = v.raw();
+  }
+}
+
+int grid_of(int64_t n) { return int(std::min<int64_t>(n, 1 << 20)); }
+
+template <typename T>
+int quant_rows(const QuantArgs& a, hipStream_t s) {
+  // A wave keeps 2048 values in registers, 256 lanes 8192.
+  if (a.pitch <= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64>), dim3(grid_of((a.rows + 3) / 4)), dim3(256), 0, s, a);
+  else if (a.pitch <= 8192) hipLaunchKernelGGL((k_quant_rows<T, 256>), dim3(grid_of(a.rows)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_quant_rows<T, 1024>), dim3(grid_of(a.rows)), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+int quant_cols(const QuantArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(k_quant_cols_max<T>, dim3(uint32_t((a.rows + 255) / 256), uint32_t(a.part_rows)), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t tiles = (a.rows + 127) / 128 * (a.pitch / 128);
+  hipLaunchKernelGGL(k_quant_cols<T>, dim3(uint32_t(tiles)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int muon_launch_quant_rows(const QuantArgs& a, bool bf16, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return bf16 ? quant_rows<uint16_t>(a, s) : quant_rows<float>(a, s);
+}
+
+int muon_launch_quant_blocks(const QuantArgs& a, bool bf16, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t total = a.rows * (a.pitch / 8);
+  const dim3 grid(grid_of((total + kUnits * 256 - 1) / (kUnits * 256)));
+  if (bf16) hipLaunchKernelGGL(k_quant_blocks<uint16_t>, grid, dim3(256), 0, s, a, total);
+  else hipLaunchKernelGGL(k_quant_blocks<float>, grid, dim3(256), 0, s, a, total);
+  return hipGetLastError();
+}
+
+int muon_launch_quant_cols(const QuantArgs& a, bool bf16, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return bf16 ? quant_cols<uint16_t>(a, s) : quant_cols<float>(a, s);
+}
+
+int muon_launch_dequant(const DequantArgs& a, bool bf16, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t total = a.rows * ((a.cols + 7) / 8);
+  const dim3 grid(grid_of((total + kUnits * 256 - 1) / (kUnits * 256)));
+  if (bf16) hipLaunchKernelGGL(k_dequant<uint16_t>, grid, dim3(256), 0, s, a, total);
+  else hipLaunchKernelGGL(k_dequant<float>, grid, dim3(256), 0, s, a, total);
+  return hipGetLastError();
+}
+
+int muon_launch_pack_rows(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int32_t cols, void* stream) {
+  const int64_t total = rows * (ldd / 8);
+  hipLaunchKernelGGL(k_pack_rows, dim3(grid_of((total + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(stream),
+                     static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), ldd, rows, cols);
+  return hipGetLastError();
+}

@@ -1,0 +1,325 @@
+// Weight gradients from 8-bit checkpoints for gfx950 (muon_linear.h): dw = dy^T x, summed over the
+// tokens, which are the rows of both operands.
+//
+// bf16 dy.  A k-step is 64 tokens.  dy's rows go straight from global memory to LDS; the codes
+// come through registers, where one token's 16 codes are decoded by its block's scale to bf16
+// (exactly) before they are written next to them.  Both lie in LDS as they lie in memory,
+// tokens as rows, and ds_read_b64_tr_b16 turns them as they are read: of each group of 16 lanes,
+// lane i gives the address of 4 columns of token i / 4, and gets 4 tokens of column i.
+//
+// fp32 dy.  v_mfma_f32_32x32x2_f32 takes one value a lane and operand, which is how the rows lie
+// in LDS already.
+#include <hip/hip_runtime.h>
+
+#include "linear_math.h"
+#include "linear_types.h"
+#include "tile_order.h"
+#include "tile_store.h"
+
+using namespace muon;
+
+namespace {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
+constexpr int kStep = 64;  // tokens of a k-step
+
+template <int n>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14));
+}
+
+// One run of 8 results: to the output, added to what is there, or to a piece's partial results.
+__device__ __forceinline__ void put8(const WgradArgs& a, int row, int col, const float (&v)[8]) {
+  if (row >= a.n || col >= a.k) return;
+  if (a.splits > 1) {
+    Eight<float>::store(a.parts + (int64_t(blockIdx.y) * a.n + row) * a.k, col, a.k, v);
+    return;
+  }
+  float f[8];
+  if (a.out_bf16) {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + int64_t(row) * a.ldo;
+    Eight<uint16_t> old;
+    old.clear();
+    if (a.accumulate) old.load(p, col, a.k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? old.get(e) + v[e] : v[e];
+    Eight<uint16_t>::store(p, col, a.k, f);
+  } else {
+    float* p = static_cast<float*>(a.out) + int64_t(row) * a.ldo;
+    Eight<float> old;
+    old.clear();
+    if (a.accumulate) old.load(p, col, a.k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? old.get(e) + v[e] : v[e];
+    Eight<float>::store(p, col, a.k, f);
+  }
+}
+
+// Place of 16-byte chunk c of token t's row in LDS.  A transposing read takes 64 bytes (4 chunks) of
+// each of 4 consecutive tokens at a time: bits 2 and 3 put these on different banks.  Bit 0 puts
+// the two chunks that a lane decodes on other banks for odd tokens than for even ones.
+__device__ __forceinline__ int place(int c, int t) { return c ^ (((t & 3) << 2) | (t & 1)); }
+
+// WM x WN waves of FM x FN results: a tile of WM FM 32 rows (columns of dy) by WN FN 32 (inputs).
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
+  constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kTM = WM * FM * 32, kTN = WN * FN * 32;
+  constexpr int kRowA = kTM * 2, kRowB = kTN * 2;  // bytes of a token's row in LDS
+  constexpr int kA = kStep * kRowA, kStage = kA + kStep * kRowB;
+  constexpr int kInstA = kA / 1024 / kWaves;                // instructions of 1 KB a wave and step
+  constexpr int kUnits = kStep * kTN / 16 / kThreads;       // 16 codes a lane and unit
+  constexpr int kPart = store_floats<FN>() * 4;
+  constexpr bool kOne = kWaves * kPart <= kStage;
+  static_assert(kInstA * 1024 * kWaves == kA && kUnits * kThreads * 16 == kStep * kTN, "whole loads per lane");
+  static_assert(kOne || kWaves / 2 * kPart <= kStage, "the stages hold the waves' parts of the store pass");
+  __shared__ __attribute__((aligned(1024))) char lds0[kStage];
+  __shared__ __attribute__((aligned(1024))) char lds1[kStage];
+
+  const int tm = (a.n + kTM - 1) / kTM, tn = (a.k + kTN - 1) / kTN;
+  int ti, tj;
+  full_band_decode(xcd_remap(int(blockIdx.x), int(gridDim.x)), tm, tn, ti, tj);
+  const int row0 = ti * kTM, col0 = tj * kTN;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WN, wn = wave % WN;
+  const int t0 = int(blockIdx.y) * a.piece, tokens = min(a.piece, a.tokens - t0);
+  const int steps = (tokens + kStep - 1) / kStep;
+
+  f32x16 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = 0.0f;
+
+  // dy: lane l of a wave's instruction fills chunk position l % (chunks a row) of one of its rows.
+  // Columns behind dy's end are clamped to its last chunk (n_read is a multiple of 8), tokens to
+  // the last token; the rows of tokens that are not there are cleared below.
+  constexpr int kChunksA = kRowA / 16, kRowsInst = 64 / kChunksA;
+  const char* dy = static_cast<const char*>(a.dy) + int64_t(t0) * a.lddy * 2;
+  int64_t src[kInstA];
+  int tok[kInstA];
+#pragma unroll
+  for (int j = 0; j < kInstA; ++j) {
+    const int t = (wave * kInstA + j) * kRowsInst + lane / kChunksA;
+    const int c = place(lane % kChunksA, t);
+    tok[j] = t;
+    src[j] = int64_t(min(row0 + c * 8, a.n_read - 8)) * 2;
+  }
+  auto load_dy = [&](int ks, char* st) {
+#pragma unroll
+    for (int j = 0; j < kInstA; ++j) {
+      const int t = min(ks * kStep + tok[j], tokens - 1);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(dy + int64_t(t) * a.lddy * 2 + src[j]),
+                                       (lds_void*)(st + (wave * kInstA + j) * 1024), 16, 0, 0);
+    }
+  };
+  // Codes: a lane has 16 codes of one token, which share a scale.
+  constexpr int kChunksB = kTN / 16;  // 16-code units of a token's row
+  u32x4 codes[kUnits];
+  float scale[kUnits];
+  auto load_x = [&](int ks) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int idx = u * kThreads + tid;
+      const int t = ks * kStep + idx / kChunksB;
+      const int col = min(col0 + idx % kChunksB * 16, a.pitch - 16);
+      const int64_t at = t0 + min(t, tokens - 1);
+      codes[u] = *(global_ptr<const u32x4>)(a.q + at * a.pitch + col);
+      scale[u] = *(global_ptr<const float>)(a.scale + at * a.groups + min(col / kCodeBlock, a.groups - 1));
+      if (t >= tokens) scale[u] = 0.0f;
+    }
+  };
+  auto put_x = [&](char* st) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int idx = u * kThreads + tid;
+      const int t = idx / kChunksB, c = idx % kChunksB * 2;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        decode8(make_uint2(codes[u][2 * h], codes[u][2 * h + 1]), scale[u], f);
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+        *reinterpret_cast<u32x4*>(st + kA + t * kRowB + place(c + h, t) * 16) = o;
+      }
+    }
+  };
+
+  // Fragments.  Of a 32 x 16 fragment (columns x tokens), lane l has column l % 32 and the tokens
+  // 8 (l / 32) .. + 7, as two transposing reads of 4.
+  const int g = lane >> 4, i16 = lane & 15;
+  auto frag_at = [&](int col) {  // byte of the first read's address within a stage's operand, less the row's
+    const int n = col + 16 * (g & 1) + (i16 & 3) * 4;
+    return place(n / 8, i16 >> 2) * 16 + (n & 4) * 2;
+  };
+  const int t_lane = 8 * (g >> 1) + (i16 >> 2);
+  int at_a[FM], at_b[FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) at_a[i] = t_lane * kRowA + frag_at((wm * FM + i) * 32);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) at_b[j] = kA + t_lane * kRowB + frag_at((wn * FN + j) * 32);
+  auto frag = [&](char* st, int at, int row_bytes, int kk) {
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(st + at + kk * 16 * row_bytes));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(st + at + (kk * 16 + 4) * row_bytes));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  auto step = [&](int ks, char* st, char* next) {
+    wait_vm<0>();
+    __syncthreads();  // dy's loads and the codes of this stage are there; the other stage is free
+    if (ks == steps - 1 && tokens % kStep) {
+      // Tokens behind the last one: x is zero there already; so that infinities in dy's last row
+      // are not multiplied with it, dy is cleared too.
+      for (int b = tokens % kStep * kRowA + tid * 16; b < kA; b += kThreads * 16) *reinterpret_cast<u32x4*>(st + b) = 0;
+      __syncthreads();
+    }
+    if (ks + 1 < steps) {
+      load_dy(ks + 1, next);
+      put_x(next);
+      if (ks + 2 < steps) load_x(ks + 2);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kStep / 16; ++kk) {
+      bf16x8 fa[FM], fb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; ++i) fa[i] = frag(st, at_a[i], kRowA, kk);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = frag(st, at_b[j], kRowB, kk);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  };
+  if (steps > 0) {
+    load_dy(0, lds0);
+    load_x(0);
+    put_x(lds0);
+    if (steps > 1) load_x(1);
+  }
+  int ks = 0;
+  for (; ks + 2 <= steps; ks += 2) {
+    step(ks, lds0, lds1);
+    step(ks + 1, lds1, lds0);
+  }
+  if (ks < steps) step(ks, lds0, lds1);
+  __syncthreads();  // the store pass uses the LDS
+
+  char* base = kOne || wave < kWaves / 2 ? lds0 : lds1;
+  float* part = reinterpret_cast<float*>(base + (kOne ? wave : wave % (kWaves / 2)) * kPart);
+  store_block(acc, part, [&](int r, int c, const float (&v)[8]) {
+    put8(a, row0 + wm * FM * 32 + r, col0 + wn * FN * 32 + c, v);
+  });
+}
+
+// fp32 dy: 128 x 128 tiles of 4 waves, 16 tokens a step, through registers.
+__global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
+  constexpr int kT = 128, kTok = 16, kLd = kT + 4;
+  __shared__ __attribute__((aligned(16))) float lds[2][2][kTok * kLd];
+  __shared__ float parts[4 * store_floats<2>()];
+  const int tm = (a.n + kT - 1) / kT, tn = (a.k + kT - 1) / kT;
+  int ti, tj;
+  full_band_decode(xcd_remap(int(blockIdx.x), int(gridDim.x)), tm, tn, ti, tj);
+  const int row0 = ti * kT, col0 = tj * kT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+  const int lr = lane & 31, lk = lane >> 5;
+  const int t0 = int(blockIdx.y) * a.piece, tokens = min(a.piece, a.tokens - t0);
+  const int steps = (tokens + kTok - 1) / kTok;
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = 0.0f;
+
+  const int t = tid >> 4, c = (tid & 15) * 8;  // a lane's token and first of 8 columns
+  Eight<float> dy;
+  uint2 codes = {};
+  float scale = 0.0f;
+  auto load = [&](int ks) {
+    const bool there = ks * kTok + t < tokens;
+    const int64_t at = t0 + min(ks * kTok + t, tokens - 1);
+    dy.clear();
+    if (there) dy.load(static_cast<const float*>(a.dy) + at * a.lddy, row0 + c, a.n);
+    const int col = min(col0 + c, a.pitch - 8);
+    codes = *reinterpret_cast<const uint2*>(a.q + at * a.pitch + col);
+    scale = there ? a.scale[at * a.groups + min(col / kCodeBlock, a.groups - 1)] : 0.0f;
+  };
+  auto put = [&](int s) {
+    float f[8];
+    decode8(codes, scale, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      lds[s][0][t * kLd + c + e] = dy.get(e);
+      lds[s][1][t * kLd + c + e] = f[e];
+    }
+  };
+  if (steps > 0) load(0);
+  for (int ks = 0; ks < steps; ++ks) {
+    put(ks & 1);
+    __syncthreads();
+    if (ks + 1 < steps) load(ks + 1);
+    const float* pa = lds[ks & 1][0] + lk * kLd + wm * 64 + lr;
+    const float* pb = lds[ks & 1][1] + lk * kLd + wn * 64 + lr;
+#pragma unroll
+    for (int kk = 0; kk < kTok / 2; ++kk) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fa[i] = pa[kk * 2 * kLd + 32 * i], fb[i] = pb[kk * 2 * kLd + 32 * i];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  store_block(acc, parts + wave * store_floats<2>(), [&](int r, int cc, const float (&v)[8]) {
+    put8(a, row0 + wm * 64 + r, col0 + wn * 64 + cc, v);
+  });
+}
+
+// Partial results of the pieces, in their order, to the output.
+__global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
+  const int chunks = (a.k + 7) / 8;
+  const int64_t total = int64_t(a.n) * chunks;
+  WgradArgs b = a;
+  b.splits = 1;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int row = int(i / chunks), col = int(i - int64_t(row) * chunks) * 8;
+    float sum[8] = {};
+    for (int s = 0; s < a.splits; ++s) {
+      Eight<float> v;
+      v.load(a.parts + (int64_t(s) * a.n + row) * a.k, col, a.k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v.get(e);
+    }
+    put8(b, row, col, sum);
+  }
+}
+
+template <int WM, int WN, int FM, int FN>
+void launch(const WgradArgs& a, hipStream_t s) {
+  const int64_t tm = (a.n + WM * FM * 32 - 1) / (WM * FM * 32), tn = (a.k + WN * FN * 32 - 1) / (WN * FN * 32);
+  hipLaunchKernelGGL((k_wgrad<WM, WN, FM, FN>), dim3(uint32_t(tm * tn), uint32_t(a.splits)), dim3(WM * WN * 64), 0, s, a);
+}
+
+}  // namespace
+
+int muon_launch_wgrad(const WgradArgs& a, bool dy_bf16, int tile, void* stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!dy_bf16) {
+    const int64_t tiles = int64_t((a.n + 127) / 128) * ((a.k + 127) / 128);
+    hipLaunchKernelGGL(k_wgrad_f32, dim3(uint32_t(tiles), uint32_t(a.splits)), dim3(256), 0, s, a);
+  } else if (tile == 256) {
+    launch<2, 4, 4, 2>(a, s);
+  } else {
+    launch<2, 2, 2, 2>(a, s);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t work = (int64_t(a.n) * ((a.k + 7) / 8) + 255) / 256;
+  hipLaunchKernelGGL(k_wgrad_join, dim3(uint32_t(work < 65536 ? work : 65536)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}

@@ -1,0 +1,297 @@
+// Host validation and planning of the 8-bit linear operators (see linear_plan.h).
+#include "linear_plan.h"
+
+#include <algorithm>
+#include <cstring>
+#include <initializer_list>
+
+#include "muon_internal.h"
+
+namespace muon {
+
+namespace {
+
+int refuse(std::string* err, int status, const std::string& what) {
+  *err = what;
+  return status;
+}
+
+int width(int32_t dtype) { return dtype == MUON_BF16 ? 2 : dtype == MUON_F32 ? 4 : 0; }
+
+// Whether two spans share a byte.  Of spans with the same step (rows of one wider buffer) the
+// columns are compared; others overlap where their whole ranges do.
+bool overlap(const Span& a, const Span& b) {
+  if (a.empty() || b.empty() || a.hi() <= b.lo || b.hi() <= a.lo) return false;
+  const bool one_row = a.rows == 1 || b.rows == 1;
+  const int64_t step = a.rows == 1 ? b.step : a.step;
+  if ((!one_row && a.step != b.step) || (a.rows == 1 && b.rows == 1)) return true;
+  // Offset of b's columns behind a's, in [0, step).
+  const int64_t d = a.lo <= b.lo ? int64_t((b.lo - a.lo) % uintptr_t(step))
+                                 : (step - int64_t((a.lo - b.lo) % uintptr_t(step))) % step;
+  return d < a.run || step - d < b.run;
+}
+
+// No output may overlap another output or an input; *b (may be NULL) keeps them all.
+int check_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins, LinearBuffers* b, std::string* err) {
+  if (b) {
+    b->count = 0;
+    for (const Span& s : outs) b->spans[b->count++] = s;
+    for (const Span& s : ins) b->spans[b->count++] = s;
+  }
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* p = o + 1; p != outs.end(); ++p)
+      if (overlap(*o, *p)) return refuse(err, MUON_EALIAS, std::string(o->name) + " overlaps " + p->name);
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return refuse(err, MUON_EALIAS, std::string(o->name) + " overlaps " + i.name);
+  }
+  return MUON_OK;
+}
+
+int check_size(const char* name, int64_t rows, int64_t cols, std::string* err) {
+  if (rows < 0 || cols < 0 || rows > kMaxLinear || cols > kMaxLinear)
+    return refuse(err, MUON_EINVAL, std::string(name) + ": rows and cols must be in [0, 2^30]");
+  return MUON_OK;
+}
+
+int check_pointer(const char* name, const void* p, uintptr_t align, int64_t bytes, std::string* err) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (!at) return refuse(err, MUON_EINVAL, std::string(name) + ": NULL pointer");
+  if (at % align) return refuse(err, MUON_EINVAL, std::string(name) + ": pointer not aligned to " + std::to_string(align) + " bytes");
+  if (uintptr_t(bytes) > UINTPTR_MAX - at) return refuse(err, MUON_EINVAL, std::string(name) + ": buffer passes the end of memory");
+  return MUON_OK;
+}
+
+int check_view(const char* name, const muon_view* v, Span* span, std::string* err) {
+  if (!v) return refuse(err, MUON_EINVAL, std::string(name) + " is NULL");
+  const int es = width(v->dtype);
+  if (!es) return refuse(err, MUON_EINVAL, std::string(name) + ": unknown dtype");
+  if (v->reserved != 0) return refuse(err, MUON_EINVAL, std::string(name) + ": reserved field must be 0");
+  const int rc = check_size(name, v->rows, v->cols, err);
+  if (rc != MUON_OK) return rc;
+  *span = {name, reinterpret_cast<uintptr_t>(v->data), v->rows, v->cols * es, v->ld * es};
+  if (span->empty()) return MUON_OK;
+  // Rows of up to 2^32 elements: any byte offset fits 64 bits.
+  if (v->rows > 1 && (v->ld < v->cols || v->ld > (int64_t(1) << 32)))
+    return refuse(err, MUON_EINVAL, std::string(name) + ": ld must be in [cols, 2^32]");
+  if (v->rows == 1) span->step = span->run;
+  return check_pointer(name, v->data, uintptr_t(es), (v->rows - 1) * span->step + span->run, err);
+}
+
+int64_t groups_of(const muon_codes& c) { return c.block ? ceil_div(c.cols, kCodeBlock) : 1; }
+
+int check_codes(const char* name, const muon_codes* c, int32_t block, Span* q, Span* scale, std::string* err) {
+  if (!c) return refuse(err, MUON_EINVAL, std::string(name) + " is NULL");
+  if (c->reserved != 0) return refuse(err, MUON_EINVAL, std::string(name) + ": reserved field must be 0");
+  if (c->block != 0 && c->block != kCodeBlock) return refuse(err, MUON_EINVAL, std::string(name) + ": block must be 0 or 128");
+  if (block >= 0 && c->block != block)
+    return refuse(err, MUON_EINVAL, std::string(name) + (block ? ": codes by block are needed" : ": codes by row are needed"));
+  int rc = check_size(name, c->rows, c->cols, err);
+  if (rc != MUON_OK) return rc;
+  const int64_t pitch = MUON_CODES_PITCH(c->cols), groups = groups_of(*c);
+  *q = {name, reinterpret_cast<uintptr_t>(c->q), c->rows, pitch, pitch};
+  *scale = {name, reinterpret_cast<uintptr_t>(c->scale), c->rows, groups * 4, groups * 4};
+  if (!q->empty() && (rc = check_pointer(name, c->q, 16, c->rows * pitch, err)) != MUON_OK) return rc;
+  if (!scale->empty() && (rc = check_pointer(name, c->scale, 4, c->rows * groups * 4, err)) != MUON_OK) return rc;
+  return MUON_OK;
+}
+
+void set_quant(const muon_view& x, bool transpose, QuantPlan* p) {
+  QuantArgs& a = p->args;
+  std::memset(&a, 0, sizeof a);
+  p->bf16 = x.dtype == MUON_BF16;
+  p->transpose = transpose;
+  p->block = 0;
+  p->buf.ws_bytes = 0;
+  a.x = x.data;
+  a.ld = x.rows > 1 ? x.ld : x.cols;
+  a.rows = transpose ? x.cols : x.rows;
+  a.cols = int32_t(transpose ? x.rows : x.cols);
+  a.pitch = int32_t(MUON_CODES_PITCH(a.cols));
+  p->buf.count = 0;
+  p->empty = a.rows == 0;
+  if (transpose && a.rows > 0 && a.cols > 0) {
+    // Strips of at least 64 rows of x, about 1024 workgroups of 256 columns, and at most 32 strips,
+    // whose maxima the second launch reads again for each of its tiles.
+    const int64_t across = ceil_div(a.rows, 256);
+    a.part_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>({ceil_div(a.cols, 64), ceil_div(1024, across), 32})));
+    p->buf.ws_bytes = size_t(a.rows) * size_t(a.part_rows) * 4;
+  }
+}
+
+}  // namespace
+
+int plan_quantize(const muon_view* x, int32_t transpose, const muon_codes* codes, QuantPlan* p, std::string* err) {
+  Span sx, q, scale;
+  int rc = check_view("x", x, &sx, err);
+  if (rc != MUON_OK) return rc;
+  if (transpose != 0 && transpose != 1) return refuse(err, MUON_EINVAL, "transpose must be 0 or 1");
+  set_quant(*x, transpose != 0, p);
+  if (!codes) return MUON_OK;
+  if ((rc = check_codes("codes", codes, transpose ? 0 : -1, &q, &scale, err)) != MUON_OK) return rc;
+  if (codes->rows != p->args.rows || codes->cols != p->args.cols)
+    return refuse(err, MUON_EINVAL, "codes must be " + std::to_string(p->args.rows) + " x " + std::to_string(p->args.cols));
+  if ((rc = check_overlap({q, scale}, {sx}, &p->buf, err)) != MUON_OK) return rc;
+  p->args.q = static_cast<int8_t*>(codes->q);
+  p->args.scale = codes->scale;
+  p->block = codes->block;
+  p->empty = scale.empty();
+  return MUON_OK;
+}
+
+int plan_dequantize(const muon_codes* codes, const muon_view* out, DequantPlan* p, std::string* err) {
+  Span q, scale, so;
+  int rc = check_codes("codes", codes, -1, &q, &scale, err);
+  if (rc != MUON_OK) return rc;
+  if ((rc = check_view("out", out, &so, err)) != MUON_OK) return rc;
+  if (out->rows != codes->rows || out->cols != codes->cols)
+    return refuse(err, MUON_EINVAL, "out must be " + std::to_string(codes->rows) + " x " + std::to_string(codes->cols));
+  if ((rc = check_overlap({so}, {q, scale}, nullptr, err)) != MUON_OK) return rc;
+  DequantArgs* a = &p->args;
+  std::memset(a, 0, sizeof *a);
+  a->q = static_cast<const int8_t*>(codes->q);
+  a->scale = codes->scale;
+  a->out = out->data;
+  a->ld = out->rows > 1 ? out->ld : out->cols;
+  a->rows = codes->rows;
+  a->cols = int32_t(codes->cols);
+  a->pitch = int32_t(MUON_CODES_PITCH(codes->cols));
+  a->block = codes->block;
+  p->bf16 = out->dtype == MUON_BF16;
+  p->empty = so.empty();
+  return MUON_OK;
+}
+
+int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, const muon_view* out, IntPlan* p,
+              std::string* err) {
+  Span sa, sas, sb, sbs, so;
+  int rc = MUON_OK;
+  if ((rc = x || !a ? check_view("x", x, &sa, err) : check_codes("a", a, 0, &sa, &sas, err)) != MUON_OK) return rc;
+  if (x) sas = {"x", 0, 0, 0, 0};
+  if ((rc = check_codes(x ? "w" : "b", b, 0, &sb, &sbs, err)) != MUON_OK) return rc;
+  const int64_t rows = x ? x->rows : a->rows, k = x ? x->cols : a->cols;
+  if (b->cols != k)
+    return refuse(err, MUON_EINVAL, "operands have " + std::to_string(k) + " and " + std::to_string(b->cols) + " columns");
+  if (k > kMaxIntSum)
+    return refuse(err, MUON_EINVAL, "more than " + std::to_string(kMaxIntSum) + " columns: sums leave 32 bits");
+  IntArgs& g = p->args;
+  std::memset(&g, 0, sizeof g);
+  g.rows = int32_t(rows);
+  g.cols = int32_t(b->rows);
+  g.k = int32_t(k);
+  g.pitch = int32_t(MUON_CODES_PITCH(k));
+  g.b = static_cast<const int8_t*>(b->q);
+  g.b_scale = b->scale;
+  p->empty = g.rows == 0 || g.cols == 0;
+  p->few = g.rows <= 16;
+  // A tile's share of its operands' reads falls with its edge; 128 fills the chip where 256 would
+  // leave compute units without a tile.
+  p->tile = ceil_div(g.rows, 256) * ceil_div(g.cols, 256) >= 192 ? 256 : 128;
+  // A launch has fewer than 2^32 lanes.
+  if (p->few ? g.cols > (1 << 26) : ceil_div(g.rows, 128) * ceil_div(g.cols, 128) > (1 << 23))
+    return refuse(err, MUON_EINVAL, "the result is too large");
+  p->quantise = false;
+  p->scale_off = p->buf.ws_bytes = 0;
+  if (x) {
+    g.x_bf16 = x->dtype == MUON_BF16;
+    g.ldx = rows > 1 ? x->ld : x->cols;
+    g.x = x->data;
+    p->quantise = !p->empty && !(p->few && g.rows * g.pitch <= 48 * 1024);
+    g.fused = !p->quantise;
+    if (p->quantise) {
+      set_quant(*x, false, &p->quant);
+      p->scale_off = size_t(round_up(rows * g.pitch, 256));
+      p->buf.ws_bytes = p->scale_off + size_t(round_up(rows * 4, 256));
+    }
+  } else {
+    g.a = static_cast<const int8_t*>(a->q);
+    g.a_scale = a->scale;
+  }
+  if (!out) return MUON_OK;
+  if ((rc = check_view("out", out, &so, err)) != MUON_OK) return rc;
+  if (out->rows != rows || out->cols != b->rows)
+    return refuse(err, MUON_EINVAL, "out must be " + std::to_string(rows) + " x " + std::to_string(b->rows));
+  if ((rc = check_overlap({so}, {sa, sas, sb, sbs}, &p->buf, err)) != MUON_OK) return rc;
+  g.out = out->data;
+  g.ldo = rows > 1 ? out->ld : out->cols;
+  g.out_bf16 = out->dtype == MUON_BF16;
+  return MUON_OK;
+}
+
+int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, int32_t accumulate, WgradPlan* p,
+               std::string* err) {
+  Span sd, sq, ss, so;
+  int rc = check_view("dy", dy, &sd, err);
+  if (rc != MUON_OK) return rc;
+  if ((rc = check_codes("x", x, kCodeBlock, &sq, &ss, err)) != MUON_OK) return rc;
+  if (dy->rows != x->rows)
+    return refuse(err, MUON_EINVAL, "dy has " + std::to_string(dy->rows) + " rows, x " + std::to_string(x->rows));
+  WgradArgs& a = p->args;
+  std::memset(&a, 0, sizeof a);
+  p->bf16 = dy->dtype == MUON_BF16;
+  a.dy = dy->data;
+  a.lddy = dy->rows > 1 ? dy->ld : dy->cols;
+  a.q = static_cast<const int8_t*>(x->q);
+  a.scale = x->scale;
+  a.tokens = int32_t(dy->rows);
+  a.n = int32_t(dy->cols);
+  a.k = int32_t(x->cols);
+  a.pitch = int32_t(MUON_CODES_PITCH(x->cols));
+  a.groups = int32_t(ceil_div(x->cols, kCodeBlock));
+  a.n_read = a.n;
+  p->empty = a.n == 0 || a.k == 0;
+  p->pack = false;
+  p->pack_ld = 0;
+  p->parts_off = p->buf.ws_bytes = 0;
+  p->tile = 128;
+  a.splits = 1;
+  a.piece = std::max(64, int32_t(round_up(a.tokens, 64)));
+  if (!p->empty) {
+    const int64_t tiles128 = ceil_div(a.n, 128) * ceil_div(a.k, 128), tiles256 = ceil_div(a.n, 256) * ceil_div(a.k, 256);
+    if (tiles128 > (1 << 23)) return refuse(err, MUON_EINVAL, "the result is too large");
+    if (p->bf16 && tiles256 >= 192) p->tile = 256;
+    const int64_t tiles = p->tile == 256 ? tiles256 : tiles128;
+    // bf16 rows go to LDS 16 bytes at a time.
+    if (p->bf16 && a.tokens > 0 && (reinterpret_cast<uintptr_t>(dy->data) % 16 || a.lddy % 8 || a.n % 8)) {
+      p->pack = true;
+      p->pack_ld = round_up(a.n, 8);
+      a.n_read = int32_t(p->pack_ld);
+      p->buf.ws_bytes = size_t(round_up(a.tokens * p->pack_ld * 2, 256));
+    }
+    // Few tiles: the tokens are cut into pieces of at least 256, about two workgroups for each
+    // compute unit in all.
+    const int64_t most = std::max<int64_t>(1, a.tokens / 256), want = ceil_div(2 * kMaxUnits, tiles);
+    if (tiles < kMaxUnits && std::min(most, want) > 1) {
+      a.piece = int32_t(round_up(ceil_div(a.tokens, std::min(most, want)), 64));
+      a.splits = int32_t(ceil_div(a.tokens, a.piece));
+    }
+    if (a.splits > 1) {
+      p->parts_off = p->buf.ws_bytes;
+      p->buf.ws_bytes += size_t(a.splits) * size_t(a.n) * size_t(a.k) * 4;
+    }
+  }
+  if (!out) return MUON_OK;
+  if ((rc = check_view("out", out, &so, err)) != MUON_OK) return rc;
+  if (accumulate != 0 && accumulate != 1) return refuse(err, MUON_EINVAL, "accumulate must be 0 or 1");
+  if (out->rows != dy->cols || out->cols != x->cols)
+    return refuse(err, MUON_EINVAL, "out must be " + std::to_string(dy->cols) + " x " + std::to_string(x->cols));
+  if ((rc = check_overlap({so}, {sd, sq, ss}, &p->buf, err)) != MUON_OK) return rc;
+  a.out = out->data;
+  a.ldo = out->rows > 1 ? out->ld : out->cols;
+  a.out_bf16 = out->dtype == MUON_BF16;
+  a.accumulate = accumulate;
+  return MUON_OK;
+}
+
+int check_linear_workspace(const LinearBuffers& b, const void* workspace, size_t bytes, std::string* err) {
+  if (b.ws_bytes == 0) return MUON_OK;
+  if (!workspace) return refuse(err, MUON_EINVAL, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return refuse(err, MUON_EINVAL, "workspace is not 256-byte aligned");
+  if (bytes < b.ws_bytes)
+    return refuse(err, MUON_ENOSPC, "workspace has " + std::to_string(bytes) + " bytes, needs " + std::to_string(b.ws_bytes));
+  const Span ws = {"workspace", reinterpret_cast<uintptr_t>(workspace), 1, int64_t(b.ws_bytes), int64_t(b.ws_bytes)};
+  for (int i = 0; i < b.count; ++i)
+    if (overlap(ws, b.spans[i])) return refuse(err, MUON_EALIAS, std::string("the workspace overlaps ") + b.spans[i].name);
+  return MUON_OK;
+}
+
+}  // namespace muon

@@ -15,7 +15,9 @@
 
 #include "../../include/muon.h"
 #include "../../include/muon_grad.h"
+#include "../../include/muon_linear.h"
 #include "../../include/muon_test_hooks.h"
+#include "linear_plan.h"
 #include "list_plan.h"
 #include "muon_internal.h"
 #include "planner.h"
@@ -143,6 +145,16 @@ int upload(int dev, const void* src, size_t bytes, void* dst, hipStream_t s) {
   if (e != hipSuccess) return hip_fail(e, "hipEventRecord (staging)");
   sl.used = true;
   return MUON_OK;
+}
+
+// f(), with an exception turned into a status: none leaves the C ABI.
+template <typename F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(MUON_EHIP, std::string("exception: ") + e.what());
+  }
 }
 
 // Caller holds g_mu.
@@ -1265,6 +1277,188 @@ int adamw_list_step_double(const adamw_list* list, const adamw_hparams_double* h
   } catch (const std::exception& e) {
     return fail(MUON_EHIP, std::string("exception: ") + e.what());
   }
+}
+
+// --- 8-bit linear operators (muon_linear.h) ---------------------------------------------
+
+namespace {
+
+// The device and stream of a call that enqueues kernels.  Caller holds g_mu.
+int linear_device(int* dev) {
+  const int rc = current_device(dev);
+  return rc != MUON_OK ? rc : check_device(*dev);
+}
+
+// Caller holds g_mu.
+int launch_quantize(int dev, hipStream_t s, const QuantPlan& p) {
+  if (p.empty) return MUON_OK;
+  const double elems = double(p.args.rows) * p.args.cols;
+  const double bytes = elems * (p.bf16 ? 2 : 4) * (p.transpose ? 2 : 1) + double(p.args.rows) * p.args.pitch;
+  if (p.block) return timed(dev, s, "quantize_blocks", 0.0, bytes, [&] { return muon_launch_quant_blocks(p.args, p.bf16, s); });
+  // Columns of no rows have no maxima: their codes are rows without codes.
+  if (p.transpose && p.args.cols > 0)
+    return timed(dev, s, "quantize_columns", 0.0, bytes, [&] { return muon_launch_quant_cols(p.args, p.bf16, s); });
+  return timed(dev, s, "quantize_rows", 0.0, bytes, [&] { return muon_launch_quant_rows(p.args, p.bf16, s); });
+}
+
+int run_int8(IntPlan& p, void* workspace, size_t workspace_bytes, void* hip_stream) {
+  std::string err;
+  int rc = check_linear_workspace(p.buf, workspace, workspace_bytes, &err);
+  if (rc != MUON_OK) return fail(rc, err);
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0;
+  if ((rc = linear_device(&dev)) != MUON_OK) return rc;
+  if (p.empty) return MUON_OK;
+  hipStream_t s = static_cast<hipStream_t>(hip_stream);
+  if (p.quantise) {
+    char* ws = static_cast<char*>(workspace);
+    p.quant.args.q = reinterpret_cast<int8_t*>(ws);
+    p.quant.args.scale = reinterpret_cast<float*>(ws + p.scale_off);
+    if ((rc = launch_quantize(dev, s, p.quant)) != MUON_OK) return rc;
+    p.args.a = p.quant.args.q;
+    p.args.a_scale = p.quant.args.scale;
+  }
+  const IntArgs& a = p.args;
+  const double flops = 2.0 * a.rows * a.cols * a.k;
+  const double bytes = (double(a.rows) + a.cols) * a.pitch + double(a.rows) * a.cols * (a.out_bf16 ? 2 : 4);
+  if (p.few) return timed(dev, s, "int8_few", flops, bytes, [&] { return muon_launch_int8_few(a, s); });
+  return timed(dev, s, "int8_product", flops, bytes, [&] { return muon_launch_int8(a, p.tile, s); });
+}
+
+}  // namespace
+
+int muon_quantize_size(const muon_view* x, int32_t transpose, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    QuantPlan p;
+    std::string err;
+    const int rc = plan_quantize(x, transpose, nullptr, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = p.buf.ws_bytes;
+    return int(MUON_OK);
+  });
+}
+
+int muon_quantize(const muon_view* x, int32_t transpose, const muon_codes* codes, void* workspace,
+                  size_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    if (!codes) return fail(MUON_EINVAL, "codes is NULL");
+    QuantPlan p;
+    std::string err;
+    int rc = plan_quantize(x, transpose, codes, &p, &err), dev = 0;
+    if (rc == MUON_OK) rc = check_linear_workspace(p.buf, workspace, workspace_bytes, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    p.args.parts = static_cast<float*>(workspace);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = linear_device(&dev)) != MUON_OK) return rc;
+    return launch_quantize(dev, static_cast<hipStream_t>(hip_stream), p);
+  });
+}
+
+int muon_dequantize(const muon_codes* codes, const muon_view* out, void* hip_stream) {
+  return guarded([&] {
+    DequantPlan p;
+    std::string err;
+    int rc = plan_dequantize(codes, out, &p, &err), dev = 0;
+    if (rc != MUON_OK) return fail(rc, err);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = linear_device(&dev)) != MUON_OK) return rc;
+    if (p.empty) return int(MUON_OK);
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    const double bytes = double(p.args.rows) * p.args.cols * (p.bf16 ? 3 : 5);
+    return timed(dev, s, "dequantize", 0.0, bytes, [&] { return muon_launch_dequant(p.args, p.bf16, s); });
+  });
+}
+
+int muon_int8_matmul_size(const muon_codes* a, const muon_codes* b, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    if (!a) return fail(MUON_EINVAL, "a is NULL");
+    IntPlan p;
+    std::string err;
+    const int rc = plan_int8(a, nullptr, b, nullptr, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = p.buf.ws_bytes;
+    return int(MUON_OK);
+  });
+}
+
+int muon_int8_matmul(const muon_codes* a, const muon_codes* b, const muon_view* out, void* workspace,
+                     size_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    if (!a || !out) return fail(MUON_EINVAL, a ? "out is NULL" : "a is NULL");
+    IntPlan p;
+    std::string err;
+    const int rc = plan_int8(a, nullptr, b, out, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    return run_int8(p, workspace, workspace_bytes, hip_stream);
+  });
+}
+
+int muon_int8_linear_size(const muon_view* x, const muon_codes* w, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    IntPlan p;
+    std::string err;
+    const int rc = plan_int8(nullptr, x, w, nullptr, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = p.buf.ws_bytes;
+    return int(MUON_OK);
+  });
+}
+
+int muon_int8_linear(const muon_view* x, const muon_codes* w, const muon_view* out, void* workspace,
+                     size_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    if (!out) return fail(MUON_EINVAL, "out is NULL");
+    IntPlan p;
+    std::string err;
+    const int rc = plan_int8(nullptr, x, w, out, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    return run_int8(p, workspace, workspace_bytes, hip_stream);
+  });
+}
+
+int muon_weight_grad_size(const muon_view* dy, const muon_codes* x, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(MUON_EINVAL, "bytes is NULL");
+    WgradPlan p;
+    std::string err;
+    const int rc = plan_wgrad(dy, x, nullptr, 0, &p, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    *bytes = p.buf.ws_bytes;
+    return int(MUON_OK);
+  });
+}
+
+int muon_weight_grad(const muon_view* dy, const muon_codes* x, const muon_view* out, int32_t accumulate,
+                     void* workspace, size_t workspace_bytes, void* hip_stream) {
+  return guarded([&] {
+    if (!out) return fail(MUON_EINVAL, "out is NULL");
+    WgradPlan p;
+    std::string err;
+    int rc = plan_wgrad(dy, x, out, accumulate, &p, &err), dev = 0;
+    if (rc == MUON_OK) rc = check_linear_workspace(p.buf, workspace, workspace_bytes, &err);
+    if (rc != MUON_OK) return fail(rc, err);
+    std::lock_guard<std::mutex> lock(g_mu);
+    if ((rc = linear_device(&dev)) != MUON_OK) return rc;
+    if (p.empty) return int(MUON_OK);
+    hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    char* ws = static_cast<char*>(workspace);
+    WgradArgs& a = p.args;
+    if (p.pack) {
+      rc = timed(dev, s, "pack_rows", 0.0, double(a.tokens) * a.n * 4,
+                 [&] { return muon_launch_pack_rows(a.dy, a.lddy, ws, p.pack_ld, a.tokens, a.n, s); });
+      if (rc != MUON_OK) return rc;
+      a.dy = ws;
+      a.lddy = p.pack_ld;
+    }
+    if (a.splits > 1) a.parts = reinterpret_cast<float*>(ws + p.parts_off);
+    const double bytes = double(a.tokens) * (double(a.n) * (p.bf16 ? 2 : 4) + a.pitch) +
+                         double(a.n) * a.k * (a.out_bf16 ? 2 : 4) * (a.accumulate ? 2 : 1);
+    return timed(dev, s, "weight_grad", 2.0 * a.tokens * a.n * a.k, bytes,
+                 [&] { return muon_launch_wgrad(a, p.bf16, p.tile, s); });
+  });
 }
 
 int muon_profile_begin(void) {
