@@ -11,6 +11,8 @@
 // in LDS already.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "linear_math.h"
 #include "linear_types.h"
 #include "tile_order.h"
@@ -30,6 +32,25 @@ constexpr int kStep = 64;  // tokens of a k-step
 template <int n>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14));
+}
+
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
+
+// Barrier of the main loop: each wave has waited for what it wrote or loaded itself, and its reads
+// of the stage before were complete when their matrix instructions ran.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>).
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
 }
 
 // One run of 8 results: to the output, added to what is there, or to a piece's partial results.
@@ -65,19 +86,32 @@ __device__ __forceinline__ void put8(const WgradArgs& a, int row, int col, const
 __device__ __forceinline__ int place(int c, int t) { return c ^ (((t & 3) << 2) | (t & 1)); }
 
 // WM x WN waves of FM x FN results: a tile of WM FM 32 rows (columns of dy) by WN FN 32 (inputs).
+//
+// dy has three stages in LDS, x two.  While step ks is multiplied, dy of step ks + 2 is on its way to
+// LDS and the codes of step ks + 2 to registers; those of step ks + 1, in registers, are decoded
+// into x's other stage between the matrix instructions.  Each stage is an array of its own, so
+// that the compiler does not take the writes of one for the loads of another.
 template <int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
+__device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kTM = WM * FM * 32, kTN = WN * FN * 32;
   constexpr int kRowA = kTM * 2, kRowB = kTN * 2;  // bytes of a token's row in LDS
-  constexpr int kA = kStep * kRowA, kStage = kA + kStep * kRowB;
+  constexpr int kA = kStep * kRowA, kB = kStep * kRowB;
   constexpr int kInstA = kA / 1024 / kWaves;                // instructions of 1 KB a wave and step
   constexpr int kUnits = kStep * kTN / 16 / kThreads;       // 16 codes a lane and unit
   constexpr int kPart = store_floats<FN>() * 4;
-  constexpr bool kOne = kWaves * kPart <= kStage;
   static_assert(kInstA * 1024 * kWaves == kA && kUnits * kThreads * 16 == kStep * kTN, "whole loads per lane");
-  static_assert(kOne || kWaves / 2 * kPart <= kStage, "the stages hold the waves' parts of the store pass");
-  __shared__ __attribute__((aligned(1024))) char lds0[kStage];
-  __shared__ __attribute__((aligned(1024))) char lds1[kStage];
+  constexpr int kGroups = kStep / 16;                       // fragment groups of 16 tokens
+  constexpr int kPieces = kUnits * 2 / kGroups;             // half units that a lane decodes with each
+  static_assert(kPieces * kGroups == kUnits * 2, "whole pieces with each fragment group");
+  // The store pass: an array each for up to a quarter of the waves.
+  constexpr int kPartWaves = (kWaves + 3) / 4;
+  constexpr int kArrA = kA > kPartWaves * kPart ? kA : kPartWaves * kPart;
+  constexpr int kArrB = kB > kPartWaves * kPart ? kB : kPartWaves * kPart;
+  __shared__ __attribute__((aligned(1024))) char a0[kArrA];
+  __shared__ __attribute__((aligned(1024))) char a1[kArrA];
+  __shared__ __attribute__((aligned(1024))) char a2[kArrA];
+  __shared__ __attribute__((aligned(1024))) char b0[kArrB];
+  __shared__ __attribute__((aligned(1024))) char b1[kArrB];
 
   const int tm = (a.n + kTM - 1) / kTM, tn = (a.k + kTN - 1) / kTN;
   int ti, tj;
@@ -96,57 +130,62 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
 
   // dy: lane l of a wave's instruction fills chunk position l % (chunks a row) of one of its rows.
   // Columns behind dy's end are clamped to its last chunk (n_read is a multiple of 8), tokens to
-  // the last token; the rows of tokens that are not there are cleared below.
+  // the last token; the rows of tokens that are not there are cleared below.  Offsets are relative
+  // to the step's first token, so they fit 32 bits.
   constexpr int kChunksA = kRowA / 16, kRowsInst = 64 / kChunksA;
   const char* dy = static_cast<const char*>(a.dy) + int64_t(t0) * a.lddy * 2;
-  int64_t src[kInstA];
-  int tok[kInstA];
+  const int ld2 = int(a.lddy * 2);
+  int src[kInstA], tok[kInstA];
 #pragma unroll
   for (int j = 0; j < kInstA; ++j) {
-    const int t = (wave * kInstA + j) * kRowsInst + lane / kChunksA;
-    const int c = place(lane % kChunksA, t);
-    tok[j] = t;
-    src[j] = int64_t(min(row0 + c * 8, a.n_read - 8)) * 2;
+    tok[j] = (wave * kInstA + j) * kRowsInst + lane / kChunksA;
+    src[j] = min(row0 + place(lane % kChunksA, tok[j]) * 8, a.n_read - 8) * 2;
   }
-  auto load_dy = [&](int ks, char* st) {
-#pragma unroll
-    for (int j = 0; j < kInstA; ++j) {
-      const int t = min(ks * kStep + tok[j], tokens - 1);
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(dy + int64_t(t) * a.lddy * 2 + src[j]),
-                                       (lds_void*)(st + (wave * kInstA + j) * 1024), 16, 0, 0);
-    }
+  auto load_dy = [&](int ks, int j, char* st) {
+    const int first = min(ks * kStep, tokens - 1), left = tokens - 1 - first;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(dy + int64_t(first) * ld2), (short)0, min(left, kStep - 1) * ld2 + a.n_read * 2, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(st + (wave * kInstA + j) * 1024), 16,
+                                             min(tok[j], left) * ld2 + src[j], 0, 0, 0);
   };
   // Codes: a lane has 16 codes of one token, which share a scale.
   constexpr int kChunksB = kTN / 16;  // 16-code units of a token's row
-  u32x4 codes[kUnits];
-  float scale[kUnits];
-  auto load_x = [&](int ks) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int idx = u * kThreads + tid;
-      const int t = ks * kStep + idx / kChunksB;
-      const int col = min(col0 + idx % kChunksB * 16, a.pitch - 16);
-      const int64_t at = t0 + min(t, tokens - 1);
-      codes[u] = *(global_ptr<const u32x4>)(a.q + at * a.pitch + col);
-      scale[u] = *(global_ptr<const float>)(a.scale + at * a.groups + min(col / kCodeBlock, a.groups - 1));
-      if (t >= tokens) scale[u] = 0.0f;
-    }
+  u32x4 xq[2][kUnits];
+  float xs[2][kUnits];
+  const int8_t* q0 = a.q + int64_t(t0) * a.pitch;
+  const float* s0 = a.scale + int64_t(t0) * a.groups;
+  const int col = min(col0 + tid % kChunksB * 16, a.pitch - 16);  // kThreads is a multiple of kChunksB
+  const int group = min(col / kCodeBlock, a.groups - 1);
+  auto load_x = [&](int ks, auto set, int u) {
+    constexpr int r = decltype(set)::value;
+    const int first = min(ks * kStep, tokens - 1);
+    const int8_t* q = q0 + int64_t(first) * a.pitch;
+    const float* s = s0 + int64_t(first) * a.groups;
+    const uint32_t t = uint32_t(min((u * kThreads + tid) / kChunksB, tokens - 1 - first));
+    xq[r][u] = *(global_ptr<const u32x4>)(q + (t * uint32_t(a.pitch) + uint32_t(col)));
+    xs[r][u] = *(global_ptr<const float>)(s + (t * uint32_t(a.groups) + uint32_t(group)));
   };
-  auto put_x = [&](char* st) {
+  // The share of a step's loads that goes with fragment group kk.  A wave's loads of 1 KB each keep
+  // the address unit busy for 16 cycles: together at the step's start, they held all waves up.
+  auto load_share = [&](int ks, int kk, char* st, auto set) {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int idx = u * kThreads + tid;
-      const int t = idx / kChunksB, c = idx % kChunksB * 2;
+    for (int j = 0; j < kInstA; ++j)
+      if (j * kGroups / kInstA == kk) load_dy(ks, j, st);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float f[8];
-        decode8(make_uint2(codes[u][2 * h], codes[u][2 * h + 1]), scale[u], f);
-        u32x4 o;
+    for (int u = 0; u < kUnits; ++u)
+      if (u * kGroups / kUnits == kk) load_x(ks, set, u);
+  };
+  // Half h of unit u, of step ks: decoded, to LDS; zero for tokens behind the last one.
+  auto put_x = [&](int ks, auto set, int u, int h, char* st) {
+    constexpr int r = decltype(set)::value;
+    const int t = (u * kThreads + tid) / kChunksB, c = tid % kChunksB * 2 + h;
+    const float s = ks * kStep + t < tokens ? xs[r][u] : 0.0f;
+    float f[8];
+    decode8(make_uint2(xq[r][u][2 * h], xq[r][u][2 * h + 1]), s, f);
+    u32x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-        *reinterpret_cast<u32x4*>(st + kA + t * kRowB + place(c + h, t) * 16) = o;
-      }
-    }
+    for (int e = 0; e < 4; ++e) o[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+    *reinterpret_cast<u32x4*>(st + t * kRowB + place(c, t) * 16) = o;
   };
 
   // Fragments.  Of a 32 x 16 fragment (columns x tokens), lane l has column l % 32 and the tokens
@@ -161,59 +200,99 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
 #pragma unroll
   for (int i = 0; i < FM; ++i) at_a[i] = t_lane * kRowA + frag_at((wm * FM + i) * 32);
 #pragma unroll
-  for (int j = 0; j < FN; ++j) at_b[j] = kA + t_lane * kRowB + frag_at((wn * FN + j) * 32);
+  for (int j = 0; j < FN; ++j) at_b[j] = t_lane * kRowB + frag_at((wn * FN + j) * 32);
   auto frag = [&](char* st, int at, int row_bytes, int kk) {
     const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(st + at + kk * 16 * row_bytes));
     const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(st + at + (kk * 16 + 4) * row_bytes));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
-  auto step = [&](int ks, char* st, char* next) {
-    wait_vm<0>();
-    __syncthreads();  // dy's loads and the codes of this stage are there; the other stage is free
-    if (ks == steps - 1 && tokens % kStep) {
-      // Tokens behind the last one: x is zero there already; so that infinities in dy's last row
-      // are not multiplied with it, dy is cleared too.
-      for (int b = tokens % kStep * kRowA + tid * 16; b < kA; b += kThreads * 16) *reinterpret_cast<u32x4*>(st + b) = 0;
+  auto load_frags = [&](char* sa, char* sb, int kk, bf16x8 (&fa)[FM], bf16x8 (&fb)[FN]) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[j] = frag(sb, at_b[j], kRowB, kk);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[i] = frag(sa, at_a[i], kRowA, kk);
+  };
+
+  // Loads are counted in their order: when step ks begins, behind dy of step ks there are codes of
+  // step ks (used already), and dy and the codes of step ks + 1 in flight: kInstA loads and 2 a
+  // unit (the barrier's empty asm statements keep a step's loads in it).  The last steps, too, load and decode what would come next (the last token, and nothing reads it): without
+  // branches the compiler mixes a step's parts, and keeps the results where they are.
+  auto step = [&](int ks, char* sa, char* sb, char* next_a, char* next_b, auto set, auto other) {
+    wait_vm<kInstA + 2 * kUnits>();
+    wait_lds();
+    stage_barrier();  // all waves' dy and codes of this step are there, and what step ks - 1 read is free
+    if (tokens - ks * kStep < kStep) {
+      // Tokens behind the last one: x is zero there; so that infinities in dy's last row are not
+      // multiplied with it, dy is cleared too.
+      for (int b = tokens % kStep * kRowA + tid * 16; b < kA; b += kThreads * 16) *reinterpret_cast<u32x4*>(sa + b) = 0;
       __syncthreads();
     }
-    if (ks + 1 < steps) {
-      load_dy(ks + 1, next);
-      put_x(next);
-      if (ks + 2 < steps) load_x(ks + 2);
-    }
-#pragma unroll
-    for (int kk = 0; kk < kStep / 16; ++kk) {
-      bf16x8 fa[FM], fb[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = frag(st, at_a[i], kRowA, kk);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = frag(st, at_b[j], kRowB, kk);
+    // The fragments of a group of 16 tokens are read while the group before is multiplied.
+    bf16x8 fa[2][FM], fb[2][FN];
+    load_frags(sa, sb, 0, fa[0], fb[0]);
+    __builtin_amdgcn_sched_barrier(0);
+    static_for<kGroups>([&](auto kc) {
+      constexpr int kk = decltype(kc)::value, cur = kk & 1;
+      constexpr bool kNext = kk + 1 < kGroups;
+      load_share(ks + 2, kk, next_a, set);
+      if constexpr (kNext) load_frags(sa, sb, kk + 1, fa[cur ^ 1], fb[cur ^ 1]);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int p = kk * kPieces; p < (kk + 1) * kPieces; ++p) put_x(ks + 1, other, p >> 1, p & 1, next_b);
+      // Between two matrix instructions: a few of the loads, the reads and the decoding's instructions.
+      static_for<FM * FN>([&](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        if constexpr (kNext) __builtin_amdgcn_sched_group_barrier(0x100, (2 * (FM + FN) + FM * FN - 1) / (FM * FN), 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      });
+      __builtin_amdgcn_sched_group_barrier(0x200, kPieces, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   if (steps > 0) {
-    load_dy(0, lds0);
-    load_x(0);
-    put_x(lds0);
-    if (steps > 1) load_x(1);
+    constexpr std::integral_constant<int, 0> x0{};
+    constexpr std::integral_constant<int, 1> x1{};
+#pragma unroll
+    for (int kk = 0; kk < kGroups; ++kk) load_share(0, kk, a0, x0);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int p = 0; p < 2 * kUnits; ++p) put_x(0, x0, p >> 1, p & 1, b0);
+#pragma unroll
+    for (int kk = 0; kk < kGroups; ++kk) load_share(1, kk, a1, x1);
+    for (int ks = 0;; ks += 6) {
+      step(ks, a0, b0, a2, b1, x0, x1);
+      if (ks + 1 >= steps) break;
+      step(ks + 1, a1, b1, a0, b0, x1, x0);
+      if (ks + 2 >= steps) break;
+      step(ks + 2, a2, b0, a1, b1, x0, x1);
+      if (ks + 3 >= steps) break;
+      step(ks + 3, a0, b1, a2, b0, x1, x0);
+      if (ks + 4 >= steps) break;
+      step(ks + 4, a1, b0, a0, b1, x0, x1);
+      if (ks + 5 >= steps) break;
+      step(ks + 5, a2, b1, a1, b0, x1, x0);
+      if (ks + 6 >= steps) break;
+    }
+    wait_vm<0>();  // what the last step loaded
   }
-  int ks = 0;
-  for (; ks + 2 <= steps; ks += 2) {
-    step(ks, lds0, lds1);
-    step(ks + 1, lds1, lds0);
-  }
-  if (ks < steps) step(ks, lds0, lds1);
   __syncthreads();  // the store pass uses the LDS
 
-  char* base = kOne || wave < kWaves / 2 ? lds0 : lds1;
-  float* part = reinterpret_cast<float*>(base + (kOne ? wave : wave % (kWaves / 2)) * kPart);
-  store_block(acc, part, [&](int r, int c, const float (&v)[8]) {
+  const int array = wave / kPartWaves;
+  char* base = array == 0 ? a0 : array == 1 ? a1 : array == 2 ? b0 : b1;
+  store_block(acc, reinterpret_cast<float*>(base + wave % kPartWaves * kPart), [&](int r, int c, const float (&v)[8]) {
     put8(a, row0 + wm * FM * 32 + r, col0 + wn * FN * 32 + c, v);
   });
+}
+
+template <int WM, int WN, int FM, int FN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
+  wgrad_tile<WM, WN, FM, FN>(a);
 }
 
 // fp32 dy: 128 x 128 tiles of 4 waves, 16 tokens a step, through registers.

@@ -14,9 +14,11 @@ typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
 template <typename T>
 using global_ptr = __attribute__((address_space(1))) T*;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Converted together, in one instruction (apart, two and two more to join them).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(lo))) |
-         uint32_t(__builtin_bit_cast(uint16_t, static_cast<__bf16>(hi))) << 16;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 // Eight consecutive values of a row, read with 16-byte accesses at any alignment of the element
