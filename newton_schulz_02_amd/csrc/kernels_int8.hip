@@ -2,10 +2,13 @@
 // and of B, both stored with the columns that are summed over contiguous and padded with zeros
 // to 128.
 //
-// Main loop: as in the bf16 products of kernels_gemm.hip (a k-step holds 128 bytes of each operand
-// row; rows go straight from global memory to LDS, two stages, 16-byte chunks swizzled by row),
-// with v_mfma_i32_32x32x32_i8: a fragment is the same 16 bytes a lane, and the sums are exact.
+// Main loop: a k-step holds 64 bytes of each operand row.  Rows go straight from global memory to
+// one of five stages in LDS, so loads have three steps to arrive, and step ks + 1 is complete
+// when step ks begins: the last group of step ks reads the first fragments of the next one, and
+// matrix instructions (v_mfma_i32_32x32x32_i8; the sums are exact) go on over the barrier.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "linear_math.h"
 #include "linear_types.h"
@@ -19,11 +22,11 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kRowBytes = 128;
+constexpr int kRowBytes = 64, kStages = 5;
 
 // Chunk position of 16-byte chunk c in LDS row r is c ^ swz(r): the 16 lanes that the LDS serves at
-// once have 16 consecutive rows at the same chunk, two of which share the 64 banks.
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+// once have 16 consecutive rows at the same chunk, four of which share the 64 banks.
+__device__ __forceinline__ int swz(int r) { return (r >> 2) & 3; }
 
 template <int n>
 __device__ __forceinline__ void wait_vm() {
@@ -38,24 +41,28 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// WM x WN waves, each with FM x FN results of 32 x 32.
-template <int WM, int WN, int FM, int FN>
+// WM x WN waves, each with FM x FN results of 32 x 32; T is the result's type.
+template <typename T, int WM, int WN, int FM, int FN>
 __device__ __forceinline__ void int8_tile(const IntArgs& a) {
   constexpr int kWaves = WM * WN, kTM = WM * FM * 32, kTN = WN * FN * 32;
   constexpr int kStage = (kTM + kTN) * kRowBytes;
-  constexpr int kInstA = kTM / 8 / kWaves, kInstB = kTN / 8 / kWaves;  // 8 rows an instruction
+  constexpr int kInstA = kTM / 16 / kWaves, kInstB = kTN / 16 / kWaves;  // 16 rows an instruction
+  constexpr int kLoads = kInstA + kInstB, kGroups = kRowBytes / 32;
   constexpr int kPart = store_floats<FN>() * 4;
-  static_assert(kInstA * 8 * kWaves == kTM && kInstB * 8 * kWaves == kTN, "whole instructions per wave");
-  static_assert(kStage * 2 >= kWaves * kPart, "the stages hold the waves' parts of the store pass");
-  static_assert(kStage % kPart == 0 || kWaves * kPart <= kStage || kWaves / 2 * kPart <= kStage, "parts lie in one stage");
-  __shared__ __attribute__((aligned(1024))) char lds0[kStage];
-  __shared__ __attribute__((aligned(1024))) char lds1[kStage];
+  constexpr int kPartWaves = (kWaves + 3) / 4;
+  static_assert(kInstA * 16 * kWaves == kTM && kInstB * 16 * kWaves == kTN, "whole instructions per wave");
+  static_assert(kStage >= kPartWaves * kPart, "a stage holds a quarter of the waves' parts of the store pass");
+  __shared__ __attribute__((aligned(1024))) char s0[kStage];
+  __shared__ __attribute__((aligned(1024))) char s1[kStage];
+  __shared__ __attribute__((aligned(1024))) char s2[kStage];
+  __shared__ __attribute__((aligned(1024))) char s3[kStage];
+  __shared__ __attribute__((aligned(1024))) char s4[kStage];
 
   const int tm = (a.rows + kTM - 1) / kTM, tn = (a.cols + kTN - 1) / kTN;
   int ti, tj;
   full_band_decode(xcd_remap(int(blockIdx.x), int(gridDim.x)), tm, tn, ti, tj);
   const int row0 = ti * kTM, col0 = tj * kTN;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, lr = lane & 31, lk = lane >> 5;
 
   i32x16 acc[FM][FN];
@@ -64,7 +71,7 @@ __device__ __forceinline__ void int8_tile(const IntArgs& a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = 0;
 
-  // Lane l of an instruction fills chunk position l % 8 of row l / 8 of its 8 rows.  Offsets are
+  // Lane l of an instruction fills chunk position l % 4 of row l / 4 of its 16 rows.  Offsets are
   // relative to the tile's first row, so they fit 32 bits whatever the operand's size; rows
   // behind the operand's end are clamped to its last one and feed results that are not stored.
   const int rows_a = min(kTM, a.rows - row0), rows_b = min(kTN, a.cols - col0);
@@ -72,81 +79,117 @@ __device__ __forceinline__ void int8_tile(const IntArgs& a) {
       const_cast<int8_t*>(a.a + int64_t(row0) * a.pitch), (short)0, rows_a * a.pitch, 0x00020000);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<int8_t*>(a.b + int64_t(col0) * a.pitch), (short)0, rows_b * a.pitch, 0x00020000);
-  uint32_t off_a[kInstA], off_b[kInstB];
+  uint32_t off[kLoads];
 #pragma unroll
-  for (int j = 0; j < kInstA; ++j) {
-    const int r = (wave * kInstA + j) * 8 + (lane >> 3);
-    off_a[j] = uint32_t(min(r, rows_a - 1) * a.pitch + (((lane & 7) ^ swz(r)) << 4));
+  for (int j = 0; j < kLoads; ++j) {
+    const int r = (j < kInstA ? wave * kInstA + j : wave * kInstB + j - kInstA) * 16 + (lane >> 2);
+    off[j] = uint32_t(min(r, (j < kInstA ? rows_a : rows_b) - 1) * a.pitch + (((lane & 3) ^ swz(r)) << 4));
   }
-#pragma unroll
-  for (int j = 0; j < kInstB; ++j) {
-    const int r = (wave * kInstB + j) * 8 + (lane >> 3);
-    off_b[j] = uint32_t(min(r, rows_b - 1) * a.pitch + (((lane & 7) ^ swz(r)) << 4));
-  }
-  auto issue = [&](int ks, char* st) {
-#pragma unroll
-    for (int j = 0; j < kInstA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (wave * kInstA + j) * 1024), 16, off_a[j],
-                                               ks * kRowBytes, 0, 0);
-#pragma unroll
-    for (int j = 0; j < kInstB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(st + kTM * kRowBytes + (wave * kInstB + j) * 1024), 16,
-                                               off_b[j], ks * kRowBytes, 0, 0);
-  };
   const int steps = a.pitch / kRowBytes;
-  auto step = [&](int ks, const char* st, char* next) {
-    wait_vm<0>();
-    stage_barrier();  // all waves' loads of this stage have landed, and the other one is free
-    if (ks + 1 < steps) issue(ks + 1, next);
-    __builtin_amdgcn_iglp_opt(1);
+  // Load j of k-step ks; steps behind the last one load that again, which nothing reads.
+  auto issue = [&](int ks, int j, char* st) {
+    const int at = min(ks, steps - 1) * kRowBytes;
+    if (j < kInstA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (wave * kInstA + j) * 1024), 16, off[j], at, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(st + kTM * kRowBytes + (wave * kInstB + j - kInstA) * 1024),
+                                               16, off[j], at, 0, 0);
+  };
+  i32x4 fa[2][FM], fb[2][FN];
+  auto read = [&](const char* st, int kk, int to) {
+    const int c = 2 * kk + lk;
 #pragma unroll
-    for (int kk = 0; kk < kRowBytes / 32; ++kk) {
-      const int c = 2 * kk + lk;
-      i32x4 fa[FM], fb[FN];
+    for (int j = 0; j < FN; ++j) {
+      const int r = (wn * FN + j) * 32 + lr;
+      fb[to][j] = *reinterpret_cast<const i32x4*>(st + kTM * kRowBytes + r * kRowBytes + ((c ^ swz(r)) << 4));
+    }
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int r = (wm * FM + i) * 32 + lr;
-        fa[i] = *reinterpret_cast<const i32x4*>(st + r * kRowBytes + ((c ^ swz(r)) << 4));
-      }
+    for (int i = 0; i < FM; ++i) {
+      const int r = (wm * FM + i) * 32 + lr;
+      fa[to][i] = *reinterpret_cast<const i32x4*>(st + r * kRowBytes + ((c ^ swz(r)) << 4));
+    }
+  };
+  // In flight when step ks begins: the loads of steps ks + 1 to ks + 3; those of ks + 1 are waited
+  // for.  Those of ks + 4 go where step ks - 1 was.
+  auto step = [&](int ks, const char* st, const char* next, char* free) {
+    wait_vm<2 * kLoads>();
+    stage_barrier();
+    static_for<kGroups>([&](auto kc) {
+      constexpr int kk = decltype(kc)::value, cur = kk & 1;
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int r = (wn * FN + j) * 32 + lr;
-        fb[j] = *reinterpret_cast<const i32x4*>(st + kTM * kRowBytes + r * kRowBytes + ((c ^ swz(r)) << 4));
-      }
+      for (int j = kk * kLoads / kGroups; j < (kk + 1) * kLoads / kGroups; ++j) issue(ks + 4, j, free);
+      if constexpr (kk + 1 < kGroups) read(st, kk + 1, cur ^ 1);
+      else read(next, 0, cur ^ 1);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-    }
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+      // Between two matrix instructions: one load and one read.
+      static_for<FM * FN>([&](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (FM + FN + FM * FN - 1) / (FM * FN), 0);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
-  if (steps > 0) issue(0, lds0);
-  int ks = 0;
-  for (; ks + 2 <= steps; ks += 2) {
-    step(ks, lds0, lds1);
-    step(ks + 1, lds1, lds0);
+  static_assert(kGroups % 2 == 0, "a step begins with the same half of the fragment registers");
+  if (steps > 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) issue(q, j, q == 0 ? s0 : q == 1 ? s1 : q == 2 ? s2 : s3);
+    wait_vm<3 * kLoads>();
+    stage_barrier();
+    read(s0, 0, 0);
+    for (int ks = 0;; ks += 5) {
+      step(ks, s0, s1, s4);
+      if (ks + 1 >= steps) break;
+      step(ks + 1, s1, s2, s0);
+      if (ks + 2 >= steps) break;
+      step(ks + 2, s2, s3, s1);
+      if (ks + 3 >= steps) break;
+      step(ks + 3, s3, s4, s2);
+      if (ks + 4 >= steps) break;
+      step(ks + 4, s4, s0, s3);
+      if (ks + 5 >= steps) break;
+    }
+    wait_vm<0>();  // what the last steps loaded
   }
-  if (ks < steps) step(ks, lds0, lds1);
   __syncthreads();  // the store pass uses the LDS
 
-  constexpr bool kOne = kWaves * kPart <= kStage;
-  char* base = kOne || wave < kWaves / 2 ? lds0 : lds1;
-  float* part = reinterpret_cast<float*>(base + (kOne ? wave : wave % (kWaves / 2)) * kPart);
-  store_block(acc, part, [&](int r, int c, const float (&v)[8]) {
-    const int row = row0 + wm * FM * 32 + r, col = col0 + wn * FN * 32 + c;
-    if (row >= a.rows || col >= a.cols) return;
-    const float sa = a.a_scale[row];
-    float f[8];
+  const int array = wave / kPartWaves;
+  char* base = array == 0 ? s0 : array == 1 ? s1 : array == 2 ? s2 : s3;
+  float* part = reinterpret_cast<float*>(base + wave % kPartWaves * kPart);
+  const int wrow = row0 + wm * FM * 32, wcol = col0 + wn * FN * 32;
+  constexpr int E = Run<T>::E;
+  const int col = wcol + store_col<FN, E>();
+  float sb[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      f[e] = float(__float_as_int(v[e])) * sa * a.b_scale[min(col + e, a.cols - 1)];
-    if (a.out_bf16) Eight<uint16_t>::store(static_cast<uint16_t*>(a.out) + int64_t(row) * a.ldo, col, a.cols, f);
-    else Eight<float>::store(static_cast<float*>(a.out) + int64_t(row) * a.ldo, col, a.cols, f);
-  });
+  for (int e = 0; e < E; ++e) sb[e] = *(global_ptr<const float>)(a.b_scale + min(col + e, a.cols - 1));
+  auto store = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    store_block<FM, FN, E>(
+        acc, part,
+        [&](int r) { return *(global_ptr<const float>)(a.a_scale + (kWhole ? wrow + r : min(wrow + r, a.rows - 1))); },
+        [&](int r, const float (&v)[E], float sa) {
+          if (!kWhole && (wrow + r >= a.rows || col >= a.cols)) return;
+          float f[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) f[e] = float(__float_as_int(v[e])) * sa * sb[e];
+          Run<T> x;
+          x.set(f);
+          x.template store<kWhole>(static_cast<T*>(a.out) + int64_t(wrow + r) * a.ldo, col, a.cols);
+        });
+  };
+  if (wrow + FM * 32 <= a.rows && wcol + FN * 32 <= a.cols) store(std::true_type{});
+  else store(std::false_type{});
 }
 
-template <int WM, int WN, int FM, int FN>
+template <typename T, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(WM * WN * 64, 1) void k_int8(IntArgs a) {
-  int8_tile<WM, WN, FM, FN>(a);
+  int8_tile<T, WM, WN, FM, FN>(a);
 }
 
 // At most 16 rows: out's columns are B's rows, read once, so the product is bound by them.  A
@@ -226,7 +269,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
 template <int WM, int WN, int FM, int FN>
 int launch(const IntArgs& a, hipStream_t s) {
   const int64_t tm = (a.rows + WM * FM * 32 - 1) / (WM * FM * 32), tn = (a.cols + WN * FN * 32 - 1) / (WN * FN * 32);
-  hipLaunchKernelGGL((k_int8<WM, WN, FM, FN>), dim3(uint32_t(tm * tn)), dim3(WM * WN * 64), 0, s, a);
+  const dim3 grid(uint32_t(tm * tn)), block(WM * WN * 64);
+  if (a.out_bf16) hipLaunchKernelGGL((k_int8<uint16_t, WM, WN, FM, FN>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_int8<float, WM, WN, FM, FN>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -44,40 +44,37 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// f(integral_constant<int, 0>) .. f(integral_constant<int, N - 1>).
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    static_for<N, I + 1>(f);
-  }
-}
-
-// One run of 8 results: to the output, added to what is there, or to a piece's partial results.
-__device__ __forceinline__ void put8(const WgradArgs& a, int row, int col, const float (&v)[8]) {
-  if (row >= a.n || col >= a.k) return;
-  if (a.splits > 1) {
-    Eight<float>::store(a.parts + (int64_t(blockIdx.y) * a.n + row) * a.k, col, a.k, v);
-    return;
-  }
-  float f[8];
-  if (a.out_bf16) {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + int64_t(row) * a.ldo;
-    Eight<uint16_t> old;
-    old.clear();
-    if (a.accumulate) old.load(p, col, a.k);
+// A wave's block of results, from row wrow and column wcol on: to the output (T), added to what is
+// there with ADD, or to a piece's partial results.
+template <typename T, bool ADD, int FM, int FN>
+__device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc)[FM][FN], float* part, int wrow, int wcol) {
+  constexpr int E = Run<T>::E;
+  const bool pieces = a.splits > 1;  // T is float then
+  T* out = pieces ? reinterpret_cast<T*>(a.parts) + int64_t(blockIdx.y) * a.n * a.k : static_cast<T*>(a.out);
+  const int64_t ld = pieces ? a.k : a.ldo;
+  const int col = wcol + store_col<FN, E>();
+  auto store = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    store_block<FM, FN, E>(
+        acc, part,
+        [&](int r) {
+          Run<T> old;
+          old.v = 0;
+          if (ADD && (kWhole || (wrow + r < a.n && col < a.k))) old.template load<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
+          return old;
+        },
+        [&](int r, const float (&v)[E], const Run<T>& old) {
+          if (!kWhole && (wrow + r >= a.n || col >= a.k)) return;
+          float f[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? old.get(e) + v[e] : v[e];
-    Eight<uint16_t>::store(p, col, a.k, f);
-  } else {
-    float* p = static_cast<float*>(a.out) + int64_t(row) * a.ldo;
-    Eight<float> old;
-    old.clear();
-    if (a.accumulate) old.load(p, col, a.k);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = a.accumulate ? old.get(e) + v[e] : v[e];
-    Eight<float>::store(p, col, a.k, f);
-  }
+          for (int e = 0; e < E; ++e) f[e] = ADD ? old.get(e) + v[e] : v[e];
+          Run<T> x;
+          x.set(f);
+          x.template store<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
+        });
+  };
+  if (wrow + FM * 32 <= a.n && wcol + FN * 32 <= a.k) store(std::true_type{});
+  else store(std::false_type{});
 }
 
 // Place of 16-byte chunk c of token t's row in LDS.  A transposing read takes 64 bytes (4 chunks) of
@@ -91,7 +88,7 @@ __device__ __forceinline__ int place(int c, int t) { return c ^ (((t & 3) << 2) 
 // LDS and the codes of step ks + 2 to registers; those of step ks + 1, in registers, are decoded
 // into x's other stage between the matrix instructions.  Each stage is an array of its own, so
 // that the compiler does not take the writes of one for the loads of another.
-template <int WM, int WN, int FM, int FN>
+template <typename T, bool ADD, int WM, int WN, int FM, int FN>
 __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kTM = WM * FM * 32, kTN = WN * FN * 32;
   constexpr int kRowA = kTM * 2, kRowB = kTN * 2;  // bytes of a token's row in LDS
@@ -285,17 +282,17 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
 
   const int array = wave / kPartWaves;
   char* base = array == 0 ? a0 : array == 1 ? a1 : array == 2 ? b0 : b1;
-  store_block(acc, reinterpret_cast<float*>(base + wave % kPartWaves * kPart), [&](int r, int c, const float (&v)[8]) {
-    put8(a, row0 + wm * FM * 32 + r, col0 + wn * FN * 32 + c, v);
-  });
+  put_block<T, ADD>(a, acc, reinterpret_cast<float*>(base + wave % kPartWaves * kPart), row0 + wm * FM * 32,
+                    col0 + wn * FN * 32);
 }
 
-template <int WM, int WN, int FM, int FN>
+template <typename T, bool ADD, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
-  wgrad_tile<WM, WN, FM, FN>(a);
+  wgrad_tile<T, ADD, WM, WN, FM, FN>(a);
 }
 
 // fp32 dy: 128 x 128 tiles of 4 waves, 16 tokens a step, through registers.
+template <typename T, bool ADD>
 __global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
   constexpr int kT = 128, kTok = 16, kLd = kT + 4;
   __shared__ __attribute__((aligned(16))) float lds[2][2][kTok * kLd];
@@ -354,19 +351,20 @@ __global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
         for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
-  store_block(acc, parts + wave * store_floats<2>(), [&](int r, int cc, const float (&v)[8]) {
-    put8(a, row0 + wm * 64 + r, col0 + wn * 64 + cc, v);
-  });
+  put_block<T, ADD>(a, acc, parts + wave * store_floats<2>(), row0 + wm * 64, col0 + wn * 64);
 }
 
 // Partial results of the pieces, in their order, to the output.
+template <typename T, bool ADD>
 __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
   const int chunks = (a.k + 7) / 8;
   const int64_t total = int64_t(a.n) * chunks;
-  WgradArgs b = a;
-  b.splits = 1;
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
     const int row = int(i / chunks), col = int(i - int64_t(row) * chunks) * 8;
+    T* out = static_cast<T*>(a.out) + int64_t(row) * a.ldo;
+    Eight<T> old;
+    old.clear();
+    if (ADD) old.load(out, col, a.k);
     float sum[8] = {};
     for (int s = 0; s < a.splits; ++s) {
       Eight<float> v;
@@ -374,31 +372,41 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v.get(e);
     }
-    put8(b, row, col, sum);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = ADD ? old.get(e) + sum[e] : sum[e];
+    Eight<T>::store(out, col, a.k, sum);
   }
 }
 
-template <int WM, int WN, int FM, int FN>
-void launch(const WgradArgs& a, hipStream_t s) {
-  const int64_t tm = (a.n + WM * FM * 32 - 1) / (WM * FM * 32), tn = (a.k + WN * FN * 32 - 1) / (WN * FN * 32);
-  hipLaunchKernelGGL((k_wgrad<WM, WN, FM, FN>), dim3(uint32_t(tm * tn), uint32_t(a.splits)), dim3(WM * WN * 64), 0, s, a);
+template <typename T, bool ADD>
+void launch(const WgradArgs& a, bool dy_bf16, int tile, hipStream_t s) {
+  const int64_t tiles = int64_t((a.n + tile - 1) / tile) * ((a.k + tile - 1) / tile);
+  const dim3 grid(uint32_t(tiles), uint32_t(a.splits));
+  if (!dy_bf16) hipLaunchKernelGGL((k_wgrad_f32<T, ADD>), grid, dim3(256), 0, s, a);
+  else if (tile == 256) hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+}
+
+template <typename T, bool ADD>
+void join(const WgradArgs& a, hipStream_t s) {
+  const int64_t work = (int64_t(a.n) * ((a.k + 7) / 8) + 255) / 256;
+  hipLaunchKernelGGL((k_wgrad_join<T, ADD>), dim3(uint32_t(work < 65536 ? work : 65536)), dim3(256), 0, s, a);
 }
 
 }  // namespace
 
 int muon_launch_wgrad(const WgradArgs& a, bool dy_bf16, int tile, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!dy_bf16) {
-    const int64_t tiles = int64_t((a.n + 127) / 128) * ((a.k + 127) / 128);
-    hipLaunchKernelGGL(k_wgrad_f32, dim3(uint32_t(tiles), uint32_t(a.splits)), dim3(256), 0, s, a);
-  } else if (tile == 256) {
-    launch<2, 4, 4, 2>(a, s);
-  } else {
-    launch<2, 2, 2, 2>(a, s);
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t work = (int64_t(a.n) * ((a.k + 7) / 8) + 255) / 256;
-  hipLaunchKernelGGL(k_wgrad_join, dim3(uint32_t(work < 65536 ? work : 65536)), dim3(256), 0, s, a);
+  const bool pieces = a.splits > 1, add = a.accumulate != 0;
+  if (pieces || (!a.out_bf16 && !add)) launch<float, false>(a, dy_bf16, tile, s);
+  else if (!a.out_bf16) launch<float, true>(a, dy_bf16, tile, s);
+  else if (add) launch<uint16_t, true>(a, dy_bf16, tile, s);
+  else launch<uint16_t, false>(a, dy_bf16, tile, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !pieces) return e;
+  if (a.out_bf16 && add) join<uint16_t, true>(a, s);
+  else if (a.out_bf16) join<uint16_t, false>(a, s);
+  else if (add) join<float, true>(a, s);
+  else join<float, false>(a, s);
   return hipGetLastError();
 }
