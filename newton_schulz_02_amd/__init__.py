@@ -18,6 +18,7 @@ Entry points mirror ``include/muon.h``: :func:`workspace_size`, :func:`muon_step
 from __future__ import annotations
 
 import ctypes
+import functools
 import json
 from ctypes import POINTER, c_char, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 from pathlib import Path
@@ -1104,6 +1105,8 @@ class Codes:
     one per row, or for codes by block one per row and 128 columns.  They are fixed at
     construction; their values may change."""
 
+    __slots__ = ("block", "shape", "device", "_memory", "_q", "_scale", "_arg")
+
     def __init__(self, q, scale, cols, *, block=False):
         import torch
 
@@ -1113,10 +1116,9 @@ class Codes:
             raise ValueError(f"q must be contiguous int8 of rows x {-(-cols // CODE_BLOCK) * CODE_BLOCK}")
         if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() != rows * groups:
             raise ValueError(f"scale must be contiguous float32 of {rows} x {groups} values")
-        _linear_device({"q": q, "scale": scale})
-        self.q, self.scale, self.block, self.shape = q, scale, bool(block), (rows, cols)
-        self.device = q.device
-        self._arg = ctypes.byref(muon_codes(q.data_ptr(), scale.data_ptr(), rows, cols, CODE_BLOCK if block else 0, 0))
+        self.device = _linear_device(q, scale)
+        self.block, self.shape, self._memory, self._q, self._scale = bool(block), (rows, cols), (q, scale), q, scale
+        self._arg = muon_codes(q.data_ptr(), scale.data_ptr(), rows, cols, CODE_BLOCK if block else 0, 0)
 
     @classmethod
     def empty(cls, rows, cols, *, block=False, device=None):
@@ -1124,35 +1126,88 @@ class Codes:
         import torch
 
         device = torch.device("cuda" if device is None else device)
-        q = torch.empty((rows, -(-cols // CODE_BLOCK) * CODE_BLOCK), dtype=torch.int8, device=device)
-        shape = (rows, -(-cols // CODE_BLOCK)) if block else (rows,)
-        return cls(q, torch.empty(shape, dtype=torch.float32, device=device), cols, block=block)
+        if device.type != "cuda":
+            raise ValueError(f"codes must be on a GPU, not on {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        return cls._empty(torch, int(rows), int(cols), bool(block), device)
+
+    @classmethod
+    def _empty(cls, torch, rows, cols, block, device):
+        # Codes and behind them the scales, in one allocation.
+        groups, self = -(-cols // CODE_BLOCK), cls.__new__(cls)
+        codes = rows * groups * CODE_BLOCK
+        memory = torch.empty(codes + 4 * rows * (groups if block else 1), dtype=torch.uint8, device=device)
+        at = memory.data_ptr()
+        self.block, self.shape, self.device, self._memory, self._q, self._scale = block, (rows, cols), device, (memory,), None, None
+        self._arg = muon_codes(at, at + codes, rows, cols, CODE_BLOCK if block else 0, 0)
+        return self
+
+    def _views(self):
+        import torch
+
+        (memory,), (rows, cols) = self._memory, self.shape
+        groups = -(-cols // CODE_BLOCK)
+        codes = rows * groups * CODE_BLOCK
+        self._q = memory[:codes].view(torch.int8).view(rows, groups * CODE_BLOCK)
+        self._scale = memory[codes:].view(torch.float32).view((rows, groups) if self.block else (rows,))
+
+    @property
+    def q(self):
+        if self._q is None:
+            self._views()
+        return self._q
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            self._views()
+        return self._scale
+
+    def record_stream(self, stream) -> None:
+        """Keep the memory until `stream` has passed what it has been given so far."""
+        for t in self._memory:
+            t.record_stream(stream)
 
     def dequantize(self, dtype=None, *, out=None, stream=None):
         """The values that the codes stand for (see :func:`dequantize`)."""
         return dequantize(self, dtype, out=out, stream=stream)
 
 
-def _linear_device(tensors):
-    """The one GPU that named tensors (or Codes) are on."""
-    device = None
-    for name, t in tensors.items():
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be on a GPU, not on {t.device}")
-        if device is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, other operands are on {device}")
-        device = t.device
+def _linear_device(first, *others):
+    """The one GPU that tensors (or Codes) are on."""
+    device = first.device
+    if device.type != "cuda":
+        raise ValueError(f"operands must be on a GPU, not on {device}")
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"operands must be on one GPU, not on {device} and {t.device}")
     return device
 
 
 def _view_arg(name, t):
     """A 2D tensor whose rows are contiguous (they may lie apart) as a muon_view."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2D")
-    (rows, cols), (ld, inner) = t.shape, t.stride()
+    (rows, cols), (ld, inner) = shape, t.stride()
     if cols > 1 and inner != 1 or rows > 1 and ld < cols:
-        raise ValueError(f"{name}: rows must be contiguous and not overlap (shape {tuple(t.shape)}, strides {t.stride()})")
-    return ctypes.byref(muon_view(t.data_ptr(), rows, cols, ld if rows > 1 else cols, _dtype_code(t), 0))
+        raise ValueError(f"{name}: rows must be contiguous and not overlap (shape {tuple(shape)}, strides {t.stride()})")
+    return muon_view(t.data_ptr(), rows, cols, ld if rows > 1 else cols, _LINEAR_TYPES.get(t.dtype) or _dtype_code(t), 0)
+
+
+class _LinearTypes(dict):
+    """dtype -> muon_dtype, filled at the first use (this module is imported without torch)."""
+
+    def get(self, dtype):
+        if not self:
+            import torch
+
+            self.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_F32})
+        return dict.get(self, dtype)
+
+
+_LINEAR_TYPES = _LinearTypes()
 
 
 def _linear_out(out, shape, dtype, default, device, stream):
@@ -1160,29 +1215,13 @@ def _linear_out(out, shape, dtype, default, device, stream):
     import torch
 
     if out is None:
-        with _on_stream(stream, device):
-            return torch.empty(shape, dtype=default if dtype is None else dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or dtype is not None and out.dtype != dtype:
-        raise ValueError(f"out must be {tuple(shape)}" + ("" if dtype is None else f" of {dtype}"))
+        if stream is None:
+            return torch.empty(shape, dtype=dtype or default, device=device)
+        with torch.cuda.stream(_linear_stream(stream, device)):
+            return torch.empty(shape, dtype=dtype or default, device=device)
+    if tuple(out.shape) != shape or dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {shape}" + ("" if dtype is None else f" of {dtype}"))
     return out
-
-
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *_):
-        return None
-
-
-_NOTHING = _Nothing()
-
-
-def _on_stream(stream, device):
-    """Where a call allocates: on the stream that it names, else on the current one."""
-    import torch
-
-    return _NOTHING if stream is None else torch.cuda.stream(_linear_stream(stream, device))
 
 
 def _linear_stream(stream, device):
@@ -1192,32 +1231,69 @@ def _linear_stream(stream, device):
     return stream
 
 
-def _linear_call(size_fn, size_args, fn, args, device, stream, tensors) -> None:
-    """fn(*args, workspace, its bytes, stream) on the operands' device, with a workspace of the size
-    that size_fn names (size_fn None: fn takes no workspace); `tensors` are what the call uses."""
+# Workspace sizes by what they depend on; the addresses here are never read.
+_ANY = 1 << 40
+
+
+@functools.lru_cache(maxsize=4096)
+def _columns_need(rows, cols, dtype) -> int:
+    need = c_size_t(0)
+    _check(lib().muon_quantize_size(muon_view(_ANY, rows, cols, cols, dtype, 0), 1, ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _matmul_need(rows, cols, k) -> int:
+    need = c_size_t(0)
+    _check(lib().muon_int8_matmul_size(muon_codes(_ANY, _ANY, rows, k, 0, 0), muon_codes(_ANY, _ANY, cols, k, 0, 0),
+                                       ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_need(rows, cols, k, dtype) -> int:
+    need = c_size_t(0)
+    _check(lib().muon_int8_linear_size(muon_view(_ANY, rows, k, k, dtype, 0), muon_codes(_ANY, _ANY, cols, k, 0, 0),
+                                       ctypes.byref(need)))
+    return need.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _weight_grad_need(tokens, outputs, ld, inputs, dtype, shift) -> int:
+    """shift: where dy begins behind a 16-byte boundary."""
+    need = c_size_t(0)
+    _check(lib().muon_weight_grad_size(muon_view(_ANY + shift, tokens, outputs, ld, dtype, 0),
+                                       muon_codes(_ANY, _ANY, tokens, inputs, CODE_BLOCK, 0), ctypes.byref(need)))
+    return need.value
+
+
+def _linear_call(fn, args, need, device, stream, tensors) -> None:
+    """fn(*args, workspace, its bytes, stream) on the operands' device, with a workspace of `need`
+    bytes (None: fn takes none); `tensors` are what the call uses."""
     import torch
 
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         with torch.cuda.device(device):
-            return _linear_call(size_fn, size_args, fn, args, device, stream, tensors)
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else \
-        _linear_stream(stream, device).cuda_stream
-    if size_fn is None:
-        _check(fn(*args, handle))
-    else:
-        need = c_size_t(0)
-        _check(size_fn(*size_args, ctypes.byref(need)))
-        if need.value:
-            # On the call's stream: its block goes to nobody else before that stream has passed.
-            with _on_stream(stream, device):
-                workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-            _check(fn(*args, workspace.data_ptr(), need.value, handle))
+            return _linear_call(fn, args, need, device, stream, tensors)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            _check(fn(*args, workspace.data_ptr(), need, handle))
         else:
-            _check(fn(*args, None, 0, handle))
-    if stream is not None:
-        for t in tensors:
-            for x in (t.q, t.scale) if isinstance(t, Codes) else (t,):
-                _keep_for(x, stream, device)
+            _check(fn(*args, handle) if need is None else fn(*args, None, 0, handle))
+        return
+    stream = _linear_stream(stream, device)
+    workspace = None
+    if need:
+        # On the call's stream: its block goes to nobody else before that stream has passed.
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    handle = stream.cuda_stream
+    _check(fn(*args, handle) if need is None else
+           fn(*args, None if workspace is None else workspace.data_ptr(), need, handle))
+    for t in tensors:
+        t.record_stream(stream)
 
 
 def quantize(x, *, block=False, transpose=False, out=None, stream=None) -> Codes:
@@ -1228,19 +1304,23 @@ def quantize(x, *, block=False, transpose=False, out=None, stream=None) -> Codes
     with the smallest power of two that fits them as the scale.  transpose=True gives the codes
     of x's columns, as rows (codes by row only): a weight's for the input gradient.  `out`: Codes
     to write to.  A row or block with a NaN or an infinity stands for NaN."""
-    device = _linear_device({"x": x} if out is None else {"x": x, "out": out})
+    import torch
+
+    device = _linear_device(x, out)
     xv = _view_arg("x", x)
-    shape = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
+    shape = (xv.cols, xv.rows) if transpose else (xv.rows, xv.cols)
     if block and transpose:
         raise ValueError("codes of columns are by row only (block=False)")
     if out is None:
-        with _on_stream(stream, device):
-            out = Codes.empty(*shape, block=block, device=device)
+        if stream is None:
+            out = Codes._empty(torch, *shape, bool(block), device)
+        else:
+            with torch.cuda.stream(_linear_stream(stream, device)):
+                out = Codes._empty(torch, *shape, bool(block), device)
     elif out.shape != shape or out.block != bool(block):
         raise ValueError(f"out must be Codes of {shape} with block={bool(block)}")
-    t = 1 if transpose else 0
-    _linear_call(lib().muon_quantize_size if t else None, (xv, t), lib().muon_quantize,
-                 (xv, t, out._arg) if t else (xv, t, out._arg, None, 0), device, stream, (x, out))
+    _linear_call(lib().muon_quantize, (xv, 1 if transpose else 0, out._arg),
+                 _columns_need(xv.rows, xv.cols, xv.dtype) if transpose else 0, device, stream, (x, out))
     return out
 
 
@@ -1248,9 +1328,9 @@ def dequantize(codes, dtype=None, *, out=None, stream=None):
     """The values that codes stand for, code * scale, in bfloat16 (default) or float32."""
     import torch
 
-    device = _linear_device({"codes": codes} if out is None else {"codes": codes, "out": out})
+    device = _linear_device(codes, out)
     out = _linear_out(out, codes.shape, dtype, torch.bfloat16, device, stream)
-    _linear_call(None, (), lib().muon_dequantize, (codes._arg, _view_arg("out", out)), device, stream, (codes, out))
+    _linear_call(lib().muon_dequantize, (codes._arg, _view_arg("out", out)), None, device, stream, (codes, out))
     return out
 
 
@@ -1259,22 +1339,22 @@ def int8_matmul(a, b, dtype=None, *, out=None, stream=None):
     32-bit integers, times the scales of token and channel, in bfloat16 (default) or float32."""
     import torch
 
-    device = _linear_device({"a": a, "b": b} if out is None else {"a": a, "b": b, "out": out})
-    out = _linear_out(out, (a.shape[0], b.shape[0]), dtype, torch.bfloat16, device, stream)
-    args = (a._arg, b._arg)
-    _linear_call(lib().muon_int8_matmul_size, args, lib().muon_int8_matmul, (*args, _view_arg("out", out)), device,
-                 stream, (a, b, out))
+    device = _linear_device(a, b, out)
+    (rows, k), cols = a.shape, b.shape[0]
+    need = _matmul_need(rows, cols, k)
+    out = _linear_out(out, (rows, cols), dtype, torch.bfloat16, device, stream)
+    _linear_call(lib().muon_int8_matmul, (a._arg, b._arg, _view_arg("out", out)), need, device, stream, (a, b, out))
     return out
 
 
 def int8_linear(x, w, dtype=None, *, out=None, stream=None):
     """int8_matmul(quantize(x), w), bit for bit, in x's dtype by default; for a few rows of x in one
     launch."""
-    device = _linear_device({"x": x, "w": w} if out is None else {"x": x, "w": w, "out": out})
-    args = (_view_arg("x", x), w._arg)
-    out = _linear_out(out, (x.shape[0], w.shape[0]), dtype, x.dtype, device, stream)
-    _linear_call(lib().muon_int8_linear_size, args, lib().muon_int8_linear, (*args, _view_arg("out", out)), device,
-                 stream, (x, w, out))
+    device = _linear_device(x, w, out)
+    xv, cols = _view_arg("x", x), w.shape[0]
+    need = _linear_need(xv.rows, cols, xv.cols, xv.dtype)
+    out = _linear_out(out, (xv.rows, cols), dtype, x.dtype, device, stream)
+    _linear_call(lib().muon_int8_linear, (xv, w._arg, _view_arg("out", out)), need, device, stream, (x, w, out))
     return out
 
 
@@ -1284,11 +1364,12 @@ def weight_grad(dy, x, dtype=None, *, out=None, accumulate=False, stream=None):
     accumulate=True it is added to `out`, the gradient so far."""
     import torch
 
-    device = _linear_device({"dy": dy, "x": x} if out is None else {"dy": dy, "x": x, "out": out})
+    device = _linear_device(dy, x, out)
     if accumulate and out is None:
         raise ValueError("accumulate needs out, the gradient to add to")
-    args = (_view_arg("dy", dy), x._arg)
-    out = _linear_out(out, (dy.shape[1], x.shape[1]), dtype, torch.float32, device, stream)
-    _linear_call(lib().muon_weight_grad_size, args, lib().muon_weight_grad,
-                 (*args, _view_arg("out", out), 1 if accumulate else 0), device, stream, (dy, x, out))
+    dv, inputs = _view_arg("dy", dy), x.shape[1]
+    need = _weight_grad_need(dv.rows, dv.cols, dv.ld, inputs, dv.dtype, (dv.data or 0) % 16)
+    out = _linear_out(out, (dv.cols, inputs), dtype, torch.float32, device, stream)
+    _linear_call(lib().muon_weight_grad, (dv, x._arg, _view_arg("out", out), 1 if accumulate else 0), need, device,
+                 stream, (dy, x, out))
     return out

@@ -192,78 +192,137 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_int8(IntArgs a) {
   int8_tile<T, WM, WN, FM, FN>(a);
 }
 
-// At most 16 rows: out's columns are B's rows, read once, so the product is bound by them.  A
-// workgroup of 8 waves takes 16 columns; wave w takes the k-steps w, w + 8, ... of 128 bytes, a
-// lane 32 bytes of one row.  Partial sums are integers and meet in LDS.  With FUSED the rows come
-// as values and every workgroup makes their codes itself, in LDS.
-constexpr int kFewRows = 16, kFewWaves = 8;
-template <bool FUSED, typename T>
+// Few rows: out's columns are B's rows, read once, so the product is bound by them.  A workgroup of
+// 8 waves takes 16 C columns and up to 16 G rows; wave w takes the k-steps w, w + 8, ... of 128
+// bytes, a lane 16 bytes of each half of one row of each operand, kAhead steps before they are
+// multiplied.
+// Partial sums are integers and meet in LDS.  With FUSED the rows come as values and every
+// workgroup makes their codes itself, in LDS, while its first loads of B are on their way.
+constexpr int kFewWaves = 8;
+template <bool FUSED, typename T, int G, int C>
 __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
+  constexpr int kAhead = C == 1 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char codes[];  // FUSED: rows x pitch
-  __shared__ int sums[kFewWaves][16][kFewRows + 1];
+  __shared__ int sums[kFewWaves][16 * C][16 * G + 1];
   __shared__ uint32_t tops[2][kFewWaves];
-  __shared__ float scales[kFewRows];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col0 = int(blockIdx.x) * 16;
+  __shared__ float scales[16 * G];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col0 = int(blockIdx.x) * 16 * C;
   const int l16 = lane & 15, part = lane >> 4;
-  const int8_t* b = a.b + int64_t(min(col0 + l16, a.cols - 1)) * a.pitch + part * 32;
   const int steps = a.pitch / 128;
-  i32x4 acc = 0;
+  const int8_t* b[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) b[c] = a.b + int64_t(min(col0 + 16 * c + l16, a.cols - 1)) * a.pitch + part * 16;
+  i32x4 w[kAhead][C][2];
+  auto load_b = [&](int ks, int u) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const global_ptr<const i32x4> p = (global_ptr<const i32x4>)(b[c] + ks * 128);
+      w[u][c][0] = __builtin_nontemporal_load(p);
+      w[u][c][1] = __builtin_nontemporal_load(p + 4);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (wave + u * kFewWaves < steps) load_b(wave + u * kFewWaves, u);
 
   if constexpr (FUSED) {
-    // The waves in groups of `team`, each with one row at a time.
+    // The waves in groups of `team`, each with one row at a time, whose first 4 chunks of 8 values a
+    // lane are kept between the maximum and the codes.
+    constexpr int kHold = 4;
     const int team = a.rows == 1 ? 8 : a.rows == 2 ? 4 : a.rows <= 4 ? 2 : 1;
     const int at_once = kFewWaves / team;
     for (int r0 = 0, turn = 0; r0 < a.rows; r0 += at_once, ++turn) {
       const int row = r0 + wave / team;
       const T* x = static_cast<const T*>(a.x) + int64_t(min(row, a.rows - 1)) * a.ldx;
       const int first = (wave % team) * 64 + lane, stride = team * 64;
+      Eight<T> v[kHold];
       uint32_t top = 0;
-      for (int c = first; c * 8 < a.pitch; c += stride) {
-        Eight<T> v;
-        v.load(x, c * 8, a.k);
-        top = max(top, v.top());
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) v[i].load(x, (first + i * stride) * 8, a.k);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) top = max(top, v[i].top());
+      for (int c = first + kHold * stride; c * 8 < a.pitch; c += stride) {
+        Eight<T> y;
+        y.load(x, c * 8, a.k);
+        top = max(top, y.top());
       }
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
-      if (lane == 0) tops[turn & 1][wave] = top;
-      __syncthreads();
-      for (int w = 0; w < team; ++w) top = max(top, tops[turn & 1][wave / team * team + w]);
+      if (team > 1) {
+        if (lane == 0) tops[turn & 1][wave] = top;
+        __syncthreads();
+        for (int i = 0; i < team; ++i) top = max(top, tops[turn & 1][wave / team * team + i]);
+      }
       if (row < a.rows) {
         const RowCoder code(top);
         if (first == 0) scales[row] = code.scale();
-        for (int c = first; c * 8 < a.pitch; c += stride) {
-          Eight<T> v;
-          v.load(x, c * 8, a.k);
-          store_codes(reinterpret_cast<int8_t*>(codes) + row * a.pitch + c * 8, code.eight(v));
+        int8_t* q = reinterpret_cast<int8_t*>(codes) + row * a.pitch;
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+          if ((first + i * stride) * 8 < a.pitch) store_codes(q + (first + i * stride) * 8, code.eight(v[i]));
+        for (int c = first + kHold * stride; c * 8 < a.pitch; c += stride) {
+          Eight<T> y;
+          y.load(x, c * 8, a.k);
+          store_codes(q + c * 8, code.eight(y));
         }
       }
     }
     __syncthreads();
   }
-  const char* mine = FUSED ? codes : reinterpret_cast<const char*>(a.a);
-  mine += min(l16, a.rows - 1) * a.pitch + part * 32;
-  for (int ks = wave; ks < steps; ks += kFewWaves) {
-    const i32x4* p = reinterpret_cast<const i32x4*>(b + ks * 128);
-    const i32x4* q = reinterpret_cast<const i32x4*>(mine + ks * 128);
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(p[0], q[0], acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(p[1], q[1], acc, 0, 0, 0);
-  }
-  // acc[r] is the sum of out's column 4 part + r (of 16) and row l16.
+  const char* rows = FUSED ? codes : reinterpret_cast<const char*>(a.a);
+  int at[G];  // few rows: 64 * 131072 bytes at most
 #pragma unroll
-  for (int r = 0; r < 4; ++r) sums[wave][4 * part + r][l16] = acc[r];
-  __syncthreads();
-  if (threadIdx.x < 16 * kFewRows) {
-    const int c = threadIdx.x & 15, row = threadIdx.x >> 4;
-    if (row < a.rows && col0 + c < a.cols) {
-      int sum = 0;
+  for (int g = 0; g < G; ++g) at[g] = min(16 * g + l16, a.rows - 1) * a.pitch + part * 16;
+  i32x4 acc[G][C];
 #pragma unroll
-      for (int w = 0; w < kFewWaves; ++w) sum += sums[w][c][row];
-      const float f = float(sum) * (FUSED ? scales[row] : a.a_scale[row]) * a.b_scale[col0 + c];
-      if (a.out_bf16) static_cast<uint16_t*>(a.out)[int64_t(row) * a.ldo + col0 + c] = uint16_t(pack_bf16(f, 0.0f));
-      else static_cast<float*>(a.out)[int64_t(row) * a.ldo + col0 + c] = f;
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[g][c] = 0;
+  for (int k0 = wave; k0 < steps; k0 += kAhead * kFewWaves) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int ks = k0 + u * kFewWaves;
+      if (ks >= steps) break;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const i32x4* q = reinterpret_cast<const i32x4*>(rows + at[g] + ks * 128);
+        const i32x4 q0 = q[0], q1 = q[4];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          acc[g][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][c][0], q0, acc[g][c], 0, 0, 0);
+          acc[g][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][c][1], q1, acc[g][c], 0, 0, 0);
+        }
+      }
+      if (ks + kAhead * kFewWaves < steps) load_b(ks + kAhead * kFewWaves, u);
     }
   }
+  // acc[g][c][r] is the sum of out's column 16 c + 4 part + r and row 16 g + l16.
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[wave][16 * c + 4 * part + r][16 * g + l16] = acc[g][c][r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * C * 16 * G; i += kFewWaves * 64) {
+    const int c = i % (16 * C), row = i / (16 * C);
+    if (row >= a.rows || col0 + c >= a.cols) continue;
+    int sum = 0;
+#pragma unroll
+    for (int v = 0; v < kFewWaves; ++v) sum += sums[v][c][row];
+    const float f = float(sum) * (FUSED ? scales[row] : a.a_scale[row]) * a.b_scale[col0 + c];
+    if (a.out_bf16) static_cast<uint16_t*>(a.out)[int64_t(row) * a.ldo + col0 + c] = uint16_t(pack_bf16(f, 0.0f));
+    else static_cast<float*>(a.out)[int64_t(row) * a.ldo + col0 + c] = f;
+  }
+}
+
+template <bool FUSED, typename T, int G, int C>
+int launch_few(const IntArgs& a, hipStream_t s) {
+  const uint32_t lds = FUSED ? uint32_t(a.rows) * uint32_t(a.pitch) : 0;
+  hipLaunchKernelGGL((k_int8_few<FUSED, T, G, C>), dim3(uint32_t((a.cols + 16 * C - 1) / (16 * C))), dim3(kFewWaves * 64),
+                     lds, s, a);
+  return hipGetLastError();
 }
 
 template <int WM, int WN, int FM, int FN>
@@ -284,10 +343,8 @@ int muon_launch_int8(const IntArgs& a, int tile, void* stream) {
 
 int muon_launch_int8_few(const IntArgs& a, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(uint32_t((a.cols + 15) / 16)), block(kFewWaves * 64);
-  const uint32_t lds = a.fused ? uint32_t(a.rows) * uint32_t(a.pitch) : 0;
-  if (!a.fused) hipLaunchKernelGGL((k_int8_few<false, float>), grid, block, 0, s, a);
-  else if (a.x_bf16) hipLaunchKernelGGL((k_int8_few<true, uint16_t>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_int8_few<true, float>), grid, block, lds, s, a);
-  return hipGetLastError();
+  if (a.fused) return a.x_bf16 ? launch_few<true, uint16_t, 1, 1>(a, s) : launch_few<true, float, 1, 1>(a, s);
+  if (a.rows <= 16) return launch_few<false, float, 1, 1>(a, s);
+  if (a.rows <= 32) return launch_few<false, float, 2, 2>(a, s);
+  return launch_few<false, float, 4, 2>(a, s);
 }

@@ -182,7 +182,7 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
   g.b = static_cast<const int8_t*>(b->q);
   g.b_scale = b->scale;
   p->empty = g.rows == 0 || g.cols == 0;
-  p->few = g.rows <= 16;
+  p->few = g.rows <= kFewRows;
   // A tile's share of its operands' reads falls with its edge; 128 fills the chip where 256 would
   // leave compute units without a tile.
   p->tile = ceil_div(g.rows, 256) * ceil_div(g.cols, 256) >= 192 ? 256 : 128;
@@ -195,7 +195,9 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
     g.x_bf16 = x->dtype == MUON_BF16;
     g.ldx = rows > 1 ? x->ld : x->cols;
     g.x = x->data;
-    p->quantise = !p->empty && !(p->few && g.rows * g.pitch <= 48 * 1024);
+    // Codes made inside the product save a launch (3 us of the host's time), but every workgroup
+    // reads x again: up to 4 rows, or 16 KB of codes.
+    p->quantise = !p->empty && !((g.rows <= 4 && g.rows * g.pitch <= 48 * 1024) || (g.rows <= 16 && g.rows * g.pitch <= 16 * 1024));
     g.fused = !p->quantise;
     if (p->quantise) {
       set_quant(*x, false, &p->quant);

@@ -49,7 +49,7 @@ int plan_dequantize(const muon_codes* codes, const muon_view* out, DequantPlan* 
 struct IntPlan {
   IntArgs args;
   bool empty;       // no result
-  bool few;         // the kernel for at most 16 rows
+  bool few;         // the kernel for at most kFewRows rows
   int tile;         // edge of a tile otherwise
   bool quantise;    // muon_int8_linear: a launch before makes the codes of x
   QuantPlan quant;  // with codes at the workspace's start, scales at scale_off

@@ -7,6 +7,7 @@
 namespace muon {
 
 constexpr int kCodeBlock = 128;         // columns of a block scale; codes' rows are padded to it
+constexpr int kFewRows = 64;              // most rows of the int8 products' kernel for few rows
 constexpr int kMaxIntSum = 131071;      // 128 * 128 * 131071 < 2^31
 
 struct QuantArgs {

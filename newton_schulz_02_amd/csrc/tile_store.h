@@ -49,7 +49,11 @@ struct Run {
   template <bool WHOLE>
   __device__ __forceinline__ void load(const T* row, int col, int cols) {
     if constexpr (WHOLE) {
-      v = *(global_ptr<const At>)(row + col);
+      // Non-temporal as the stores, but not for bf16, where a run is half of what the lane beside it
+      // will ask for again (an fp32 gradient of 4096 x 4096 added to: 33.4 -> 30.0 us for 128
+      // tokens; a bf16 one 16.5 -> 17.9).
+      if constexpr (sizeof(T) == 4) v = __builtin_nontemporal_load((global_ptr<const At>)(row + col));
+      else v = *(global_ptr<const At>)(row + col);
     } else {
       v = 0;
 #pragma unroll
@@ -63,7 +67,7 @@ struct Run {
   template <bool WHOLE>
   __device__ __forceinline__ void store(T* row, int col, int cols) const {
     if constexpr (WHOLE) {
-      *(global_ptr<At>)(row + col) = v;
+      __builtin_nontemporal_store(v, (global_ptr<At>)(row + col));
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)

@@ -197,7 +197,7 @@ def test_views_of_single_rows_and_columns():
     x = torch.zeros(6, 8)
     for t, want in ((x[:, 2:5], (6, 3, 8)), (x[:1].expand(1, 8), (1, 8, 8)), (x[:, :1], (6, 1, 8)),
                     (x[::2], (3, 8, 16)), (x[2:2], (0, 8, 8))):
-        v = nm._view_arg("x", t)._obj
+        v = nm._view_arg("x", t)
         assert (v.rows, v.cols, v.ld) == want and v.dtype == nm.MUON_F32
 
 
