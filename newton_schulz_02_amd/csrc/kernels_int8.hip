@@ -257,14 +257,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
       if (row < a.rows) {
         const RowCoder code(top);
         if (first == 0) scales[row] = code.scale();
-        int8_t* q = reinterpret_cast<int8_t*>(codes) + row * a.pitch;
+        uint2* q = reinterpret_cast<uint2*>(codes + row * a.pitch);
 #pragma unroll
         for (int i = 0; i < kHold; ++i)
-          if ((first + i * stride) * 8 < a.pitch) store_codes(q + (first + i * stride) * 8, code.eight(v[i]));
+          if ((first + i * stride) * 8 < a.pitch) q[first + i * stride] = code.eight(v[i]);
         for (int c = first + kHold * stride; c * 8 < a.pitch; c += stride) {
           Eight<T> y;
           y.load(x, c * 8, a.k);
-          store_codes(q + c * 8, code.eight(y));
+          q[c] = code.eight(y);
         }
       }
     }

@@ -7,6 +7,7 @@
 
 #include "linear_math.h"
 #include "linear_types.h"
+#include "tile_store.h"
 
 using namespace muon;
 
@@ -20,13 +21,12 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return v;
 }
 
-// Codes of rows.  L lanes take a row together: a wave (short rows, four to a workgroup), or a
-// workgroup of 256 or 1024 lanes.  The first kKeep chunks of 8 values of each lane stay in
-// registers between the maximum and the codes; longer rows are read again (they come from L2).
-constexpr int kKeep = 4;
-template <typename T, int L>
+// Codes of rows.  L lanes take a row together: a wave (four rows to a workgroup), or a workgroup of
+// 256 or 1024 lanes.  The first KEEP chunks of 8 values of each lane stay in registers between the
+// maximum and the codes; longer rows are read again (they come from L2).
+template <typename T, int L, int KEEP>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
-  constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L;
+  constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L, kKeep = KEEP;
   __shared__ uint32_t tops[2][L > 64 ? L / 64 : 1];
   const int lane = threadIdx.x % L;
   const int chunks = a.pitch / 8;
@@ -162,13 +162,10 @@ __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const RowCoder code(max(tops[0][lane * 8 + e], tops[1][lane * 8 + e]));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w |= uint32_t(code.one(v[4 * h + j].get(e)) & 255) << (8 * j);
-      tile[(lane * 8 + e) * 33 + h * 16 + sub] = w;
-    }
+    uint32_t w[2];
+    code.codes<8>(w, [&](int u) { return v[u].get(e); });
+    tile[(lane * 8 + e) * 33 + sub] = w[0];
+    tile[(lane * 8 + e) * 33 + 16 + sub] = w[1];
   }
   __syncthreads();
   if (r0 == 0 && threadIdx.x < 128 && c0 + int(threadIdx.x) < cols)
@@ -182,14 +179,16 @@ __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
   }
 }
 
-// Values of codes: a lane takes 8 of one row.
+// Values of codes: a lane takes 16 bytes of the result, 8 or 4 codes of one row, so that a wave
+// writes whole lines.
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequant(DequantArgs a, int64_t total) {
-  const int chunks = (a.cols + 7) / 8;
+  constexpr int E = Run<T>::E;
+  const int chunks = (a.cols + E - 1) / E;
   for (int64_t base = int64_t(blockIdx.x) * (kUnits * 256); base < total; base += int64_t(gridDim.x) * (kUnits * 256)) {
     const int64_t row0 = base / chunks;
     const int c0 = int(base - row0 * chunks);
-    uint2 q[kUnits];
+    uint32_t q[kUnits][E / 4];
     float s[kUnits];
     int64_t row[kUnits];
     int c[kUnits];
@@ -197,18 +196,25 @@ __global__ __launch_bounds__(256) void k_dequant(DequantArgs a, int64_t total) {
     for (int u = 0; u < kUnits; ++u) {
       const int at = c0 + u * 256 + int(threadIdx.x);
       row[u] = row0 + at / chunks;
-      c[u] = at % chunks;
+      c[u] = at % chunks * E;
       if (row[u] < a.rows) {
-        q[u] = *reinterpret_cast<const uint2*>(a.q + row[u] * a.pitch + c[u] * 8);
-        s[u] = a.block ? a.scale[row[u] * ((a.cols + kCodeBlock - 1) / kCodeBlock) + c[u] / 16] : a.scale[row[u]];
+        const int8_t* p = a.q + row[u] * a.pitch + c[u];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) q[u][i] = reinterpret_cast<const uint32_t*>(p)[i];
+        s[u] = a.block ? a.scale[row[u] * ((a.cols + kCodeBlock - 1) / kCodeBlock) + c[u] / kCodeBlock] : a.scale[row[u]];
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
       if (row[u] < a.rows) {
-        float f[8];
-        decode8(q[u], s[u], f);
-        Eight<T>::store(static_cast<T*>(a.out) + row[u] * a.ld, c[u] * 8, a.cols, f);
+        float f[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = code_of(q[u][e / 4], e % 4) * s[u];
+        Run<T> x;
+        x.set(f);
+        T* out = static_cast<T*>(a.out) + row[u] * a.ld;
+        if (c[u] + E <= a.cols) x.template store<true>(out, c[u], a.cols);
+        else x.template store<false>(out, c[u], a.cols);
       }
   }
 }
@@ -231,10 +237,14 @@ int grid_of(int64_t n) { return int(std::min<int64_t>(n, 1 << 20)); }
 
 template <typename T>
 int quant_rows(const QuantArgs& a, hipStream_t s) {
-  // A wave keeps 2048 values in registers, 256 lanes 8192.
-  if (a.pitch <= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64>), dim3(grid_of((a.rows + 3) / 4)), dim3(256), 0, s, a);
-  else if (a.pitch <= 8192) hipLaunchKernelGGL((k_quant_rows<T, 256>), dim3(grid_of(a.rows)), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_quant_rows<T, 1024>), dim3(grid_of(a.rows)), dim3(1024), 0, s, a);
+  // A wave keeps 1024 or 4096 values in registers, 256 lanes 16384.  With a wave a row nothing waits
+  // at barriers; where that leaves compute units without one, 256 lanes are done sooner.
+  const dim3 waves(grid_of((a.rows + 3) / 4)), groups(grid_of(a.rows));
+  if (a.pitch <= 1024) hipLaunchKernelGGL((k_quant_rows<T, 64, 2>), waves, dim3(256), 0, s, a);
+  else if (a.pitch <= 4096 && a.rows >= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64, 8>), waves, dim3(256), 0, s, a);
+  else if (a.pitch <= 4096) hipLaunchKernelGGL((k_quant_rows<T, 256, 2>), groups, dim3(256), 0, s, a);
+  else if (a.pitch <= 16384) hipLaunchKernelGGL((k_quant_rows<T, 256, 8>), groups, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_quant_rows<T, 1024, 4>), groups, dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
@@ -271,7 +281,7 @@ int muon_launch_quant_cols(const QuantArgs& a, bool bf16, void* stream) {
 
 int muon_launch_dequant(const DequantArgs& a, bool bf16, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int64_t total = a.rows * ((a.cols + 7) / 8);
+  const int64_t total = a.rows * (bf16 ? (a.cols + 7) / 8 : (a.cols + 3) / 4);
   const dim3 grid(grid_of((total + kUnits * 256 - 1) / (kUnits * 256)));
   if (bf16) hipLaunchKernelGGL(k_dequant<uint16_t>, grid, dim3(256), 0, s, a, total);
   else hipLaunchKernelGGL(k_dequant<float>, grid, dim3(256), 0, s, a, total);

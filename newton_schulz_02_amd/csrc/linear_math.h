@@ -11,6 +11,7 @@ namespace muon {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
 typedef u32x4 __attribute__((aligned(4))) u32x4_at4;
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 template <typename T>
 using global_ptr = __attribute__((address_space(1))) T*;
 
@@ -55,7 +56,7 @@ struct Eight<uint16_t> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
     if (at + 8 <= cols) {
-      *(global_ptr<u32x4_at2>)(row + at) = o;
+      __builtin_nontemporal_store(o, (global_ptr<u32x4_at2>)(row + at));
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -105,38 +106,67 @@ struct Eight<float> {
   }
 };
 
-__device__ __forceinline__ void store_codes(int8_t* q, uint2 codes) { *reinterpret_cast<uint2*>(q) = codes; }
+// Codes to global memory.
+__device__ __forceinline__ void store_codes(int8_t* q, uint2 codes) { __builtin_nontemporal_store(u32x2{codes.x, codes.y}, (global_ptr<u32x2>)(q)); }
 
-// Codes of a row from the bits of its largest magnitude.  The nearest integer to 127 x / max is
-// that of x (127 / max), whose two roundings move it by less than 127 * 2^-23 < 2^-16, unless
-// the result lies that near to the middle between two integers: there 127 |x| is compared with
-// max times the middle, both exact in 64 bits (24 + 7 and 24 + 8 bits).
+// Low bytes of four words, as one.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+  return lo | hi;
+}
+
+// 3 * 2^22: a float from 2^23 to 2^24 has steps of 1, so the sum of this and a small value rounds to
+// an integer, ties to even, and its low byte is that integer's.
+constexpr float kToInt = 12582912.0f;
+
+// Codes of a row from the bits of its largest magnitude.  The nearest integer n to 127 x / max is
+// that of x (127 / max), whose error is below 127 * 2^-24 < 2^-17, unless it lies that near to the
+// middle between two integers.  A group of codes with one that comes within 2^-14 of it is made
+// again: 127 |x| is compared with max times the middle, both exact in 64 bits (24 + 7 and 24 + 8
+// bits).
 struct RowCoder {
-  float size, up, inverse;  // up: tiny rows are scaled first, so that 127 / max stays finite
-  bool lost;                // a NaN or an infinity
+  float size, inverse;
+  bool lost;  // a NaN or an infinity
+  bool tiny;  // scaled by 2^100 first, so that 127 / max stays finite
   __device__ __forceinline__ explicit RowCoder(uint32_t top) {
     lost = top >= 0x7f800000u;
     size = lost ? 0.0f : __uint_as_float(top);
-    up = size < 0x1p-100f ? 0x1p100f : 1.0f;
-    inverse = size > 0.0f ? 127.0f / (size * up) : 0.0f;
+    tiny = size < 0x1p-100f;
+    inverse = size > 0.0f ? 127.0f / (tiny ? size * 0x1p100f : size) : 0.0f;
   }
   __device__ __forceinline__ float scale() const { return lost ? __uint_as_float(0x7fc00000u) : size / 127.0f; }
-  __device__ __forceinline__ int one(float x) const {
-    const float y = (x * up) * inverse;
+  __device__ __forceinline__ uint32_t exact(float x) const {
+    const float y = (tiny ? x * 0x1p100f : x) * inverse;
     float n = rintf(y);
-    if (fabsf(y - n) > 0.5f - 0x1p-14f) {
+    if (fabsf(y - n) > 0.5f - 0x1p-13f) {
       const float low = floorf(fabsf(y));
       const double have = fabs(double(x)) * 127.0, middle = double(size) * (double(low) + 0.5);
-      const bool up_one = have > middle || (have == middle && (int(low) & 1));
-      n = copysignf(up_one ? low + 1.0f : low, x);
+      n = copysignf(have > middle || (have == middle && (int(low) & 1)) ? low + 1.0f : low, x);
     }
-    return lost ? 0 : int(n);
+    return uint32_t(int(n));
+  }
+  // The codes of N values (a multiple of 4), x(0) .. x(N - 1).
+  template <int N, typename X>
+  __device__ __forceinline__ void codes(uint32_t (&w)[N / 4], X&& x) const {
+    uint32_t n[N];
+    float near = tiny ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float r = fmaf(x(i), inverse, kToInt);
+      near = fmaxf(near, fabsf(fmaf(x(i), inverse, kToInt - r)));
+      n[i] = __float_as_uint(r);
+    }
+    if (near > 0.5f - 0x1p-14f) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) n[i] = exact(x(i));
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = lost ? 0u : low_bytes(n[4 * i], n[4 * i + 1], n[4 * i + 2], n[4 * i + 3]);
   }
   template <typename V>
   __device__ __forceinline__ uint2 eight(const V& v) const {
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e / 4] |= uint32_t(one(v.get(e)) & 255) << (8 * (e % 4));
+    uint32_t w[2];
+    codes<8>(w, [&](int e) { return v.get(e); });
     return make_uint2(w[0], w[1]);
   }
 };
@@ -155,20 +185,19 @@ struct BlockCoder {
   template <typename V>
   __device__ __forceinline__ uint2 eight(const V& v) const {
     const float inverse = __uint_as_float(uint32_t(127 - e) << 23);
-    uint32_t w[2] = {0, 0};
+    uint32_t n[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = rintf(fminf(fmaxf(v.get(i) * inverse, -127.0f), 127.0f));
-      w[i / 4] |= uint32_t((lost ? 0 : int(n)) & 255) << (8 * (i % 4));
-    }
-    return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 8; ++i) n[i] = __float_as_uint(__builtin_amdgcn_fmed3f(v.get(i) * inverse, -127.0f, 127.0f) + kToInt);
+    return make_uint2(lost ? 0u : low_bytes(n[0], n[1], n[2], n[3]), lost ? 0u : low_bytes(n[4], n[5], n[6], n[7]));
   }
 };
 
+// Code e (0..3) of a word.
+__device__ __forceinline__ float code_of(uint32_t w, int e) { return float(int32_t(w << (24 - 8 * e)) >> 24); }
+
 __device__ __forceinline__ void decode8(uint2 q, float s, float (&f)[8]) {
-  const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = float(int32_t(w[e / 4] << (24 - 8 * (e % 4))) >> 24) * s;
+  for (int e = 0; e < 8; ++e) f[e] = code_of(e < 4 ? q.x : q.y, e % 4) * s;
 }
 
 }  // namespace muon
