@@ -237,16 +237,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
       const T* x = static_cast<const T*>(a.x) + int64_t(min(row, a.rows - 1)) * a.ldx;
       const int first = (wave % team) * 64 + lane, stride = team * 64;
       Eight<T> v[kHold];
-      uint32_t top = 0;
+      typename Eight<T>::Tops tops_of;
 #pragma unroll
       for (int i = 0; i < kHold; ++i) v[i].load(x, (first + i * stride) * 8, a.k);
 #pragma unroll
-      for (int i = 0; i < kHold; ++i) top = max(top, v[i].top());
+      for (int i = 0; i < kHold; ++i) tops_of.take(v[i]);
       for (int c = first + kHold * stride; c * 8 < a.pitch; c += stride) {
         Eight<T> y;
         y.load(x, c * 8, a.k);
-        top = max(top, y.top());
+        tops_of.take(y);
       }
+      uint32_t top = tops_of.all();
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
       if (team > 1) {

@@ -34,17 +34,17 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
   for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / L; row < a.rows; row += int64_t(gridDim.x) * kRows) {
     const T* x = static_cast<const T*>(a.x) + row * a.ld;
     Eight<T> v[kKeep];
-    uint32_t top = 0;
+    typename Eight<T>::Tops tops_of;
 #pragma unroll
     for (int i = 0; i < kKeep; ++i) v[i].load(x, (lane + i * L) * 8, a.cols);
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) top = max(top, v[i].top());
+    for (int i = 0; i < kKeep; ++i) tops_of.take(v[i]);
     for (int c = lane + kKeep * L; c < chunks; c += L) {
       Eight<T> w;
       w.load(x, c * 8, a.cols);
-      top = max(top, w.top());
+      tops_of.take(w);
     }
-    top = lanes_max<64>(top);
+    uint32_t top = lanes_max<64>(tops_of.all());
     if constexpr (L > 64) {
       // The two halves of `tops` take turns, so one barrier a row is enough.
       if ((threadIdx.x & 63) == 0) tops[turn & 1][threadIdx.x / 64] = top;
@@ -89,7 +89,9 @@ __global__ __launch_bounds__(256) void k_quant_blocks(QuantArgs a, int64_t total
     }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const uint32_t top = lanes_max<16>(v[u].top());
+      typename Eight<T>::Tops tops;
+      tops.take(v[u]);
+      const uint32_t top = lanes_max<16>(tops.all());
       if (row[u] >= a.rows) continue;
       const BlockCoder code(top);
       store_codes(a.q + row[u] * a.pitch + c[u] * 8, code.eight(v[u]));
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(256) void k_quant_cols_max(QuantArgs a) {
   const int strip = (rows + a.part_rows - 1) / a.part_rows;
   const int lo = int(blockIdx.y) * strip, hi = min(rows, lo + strip);
   const int col = int(blockIdx.x) * 256 + lane * 8;
-  uint32_t top[8] = {};
+  typename Eight<T>::Tops top;
   for (int r = lo + sub; r < hi; r += 32) {
     Eight<T> v[4];
 #pragma unroll
@@ -119,12 +121,10 @@ __global__ __launch_bounds__(256) void k_quant_cols_max(QuantArgs a) {
       if (r + 8 * u < hi) v[u].load(static_cast<const T*>(a.x) + int64_t(r + 8 * u) * a.ld, col, cols);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top[e] = max(top[e], v[u].bits(e));
+    for (int u = 0; u < 4; ++u) top.take(v[u]);
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) tops[sub][lane * 8 + e] = top[e];
+  for (int e = 0; e < 8; ++e) tops[sub][lane * 8 + e] = top.get(e);
   __syncthreads();
   const int c = threadIdx.x;
   uint32_t t = 0;
@@ -237,11 +237,10 @@ int grid_of(int64_t n) { return int(std::min<int64_t>(n, 1 << 20)); }
 
 template <typename T>
 int quant_rows(const QuantArgs& a, hipStream_t s) {
-  // A wave keeps 1024 or 4096 values in registers, 256 lanes 16384.  With a wave a row nothing waits
-  // at barriers; where that leaves compute units without one, 256 lanes are done sooner.
+  // A wave keeps 1024 values in registers, 256 lanes 4096 or 16384.  (A wave for each row of 4096, 8
+  // chunks a lane, took 24.9 us for 8192 bf16 rows; 256 lanes take 20.6.)
   const dim3 waves(grid_of((a.rows + 3) / 4)), groups(grid_of(a.rows));
   if (a.pitch <= 1024) hipLaunchKernelGGL((k_quant_rows<T, 64, 2>), waves, dim3(256), 0, s, a);
-  else if (a.pitch <= 4096 && a.rows >= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64, 8>), waves, dim3(256), 0, s, a);
   else if (a.pitch <= 4096) hipLaunchKernelGGL((k_quant_rows<T, 256, 2>), groups, dim3(256), 0, s, a);
   else if (a.pitch <= 16384) hipLaunchKernelGGL((k_quant_rows<T, 256, 8>), groups, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_quant_rows<T, 1024, 4>), groups, dim3(1024), 0, s, a);
