@@ -339,7 +339,8 @@ int launch(const IntArgs& a, hipStream_t s) {
 
 int muon_launch_int8(const IntArgs& a, int tile, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return tile == 256 ? launch<2, 4, 4, 2>(a, s) : launch<2, 2, 2, 2>(a, s);
+  if (tile == kTile256) return launch<2, 4, 4, 2>(a, s);
+  return tile == kTile256x128 ? launch<4, 2, 2, 2>(a, s) : launch<2, 2, 2, 2>(a, s);
 }
 
 int muon_launch_int8_few(const IntArgs& a, void* stream) {

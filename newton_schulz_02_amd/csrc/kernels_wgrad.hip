@@ -366,11 +366,17 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
     old.clear();
     if (ADD) old.load(out, col, a.k);
     float sum[8] = {};
-    for (int s = 0; s < a.splits; ++s) {
-      Eight<float> v;
-      v.load(a.parts + (int64_t(s) * a.n + row) * a.k, col, a.k);
+    for (int s0 = 0; s0 < a.splits; s0 += 4) {  // four pieces' loads in flight
+      Eight<float> v[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += v.get(e);
+      for (int s = 0; s < 4; ++s) {
+        v[s].clear();
+        if (s0 + s < a.splits) v[s].load(a.parts + (int64_t(s0 + s) * a.n + row) * a.k, col, a.k);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[s].get(e);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = ADD ? old.get(e) + sum[e] : sum[e];
@@ -380,10 +386,11 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
 
 template <typename T, bool ADD>
 void launch(const WgradArgs& a, bool dy_bf16, int tile, hipStream_t s) {
-  const int64_t tiles = int64_t((a.n + tile - 1) / tile) * ((a.k + tile - 1) / tile);
+  const int edge = tile == kTile256 ? 256 : 128;
+  const int64_t tiles = int64_t((a.n + edge - 1) / edge) * ((a.k + edge - 1) / edge);
   const dim3 grid(uint32_t(tiles), uint32_t(a.splits));
   if (!dy_bf16) hipLaunchKernelGGL((k_wgrad_f32<T, ADD>), grid, dim3(256), 0, s, a);
-  else if (tile == 256) hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+  else if (tile == kTile256) hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
 }
 

@@ -118,6 +118,34 @@ void set_quant(const muon_view& x, bool transpose, QuantPlan* p) {
   }
 }
 
+// Few tiles: the tokens are cut into pieces, whose partial results a second launch joins.  In
+// microseconds: a step of 64 tokens takes 0.66 where the workgroups share no compute unit, a join
+// 3, a tenth for each piece and its bytes at 5 TB/s.
+int32_t wgrad_splits(int64_t tiles, const WgradArgs& a) {
+  const double steps = double(ceil_div(a.tokens, 64)), bytes = 8.0 * a.n * a.k;
+  double best = 0.66 * steps * std::max(1.0, double(tiles) / 384);
+  int32_t splits = 1;
+  for (int32_t s = 2; s <= 64 && s <= steps / 2 && tiles * s <= 3 * kMaxUnits; ++s) {
+    const double t = 0.66 * double(ceil_div(int64_t(steps), s)) * std::max(1.0, double(tiles * s) / 384) + 3.0 + 0.1 * s +
+                     s * bytes / 5e6;
+    if (t < best) best = t, splits = s;
+  }
+  return splits;
+}
+
+// Which tile: the fewest rounds over the compute units, weighed by what a round takes.  A tile's
+// share of its operands' reads falls with its edges, so a smaller one takes more than its share of
+// a 256 x 256 tile's time: measured per round of FILL.
+int int8_tile(int64_t rows, int64_t cols) {
+  const int64_t full = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 256), kMaxUnits);
+  const int64_t half = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 128), kMaxUnits);
+  const int64_t tiles = ceil_div(rows, 128) * ceil_div(cols, 128);
+  const double t256 = 1.0 * full, t256x128 = 0.56 * half;
+  const double t128 = tiles <= kMaxUnits ? 0.33 : 0.62 * ceil_div(tiles, 2 * kMaxUnits);
+  if (t256 <= t256x128 && t256 <= t128) return kTile256;
+  return t256x128 <= t128 ? kTile256x128 : kTile128;
+}
+
 }  // namespace
 
 int plan_quantize(const muon_view* x, int32_t transpose, const muon_codes* codes, QuantPlan* p, std::string* err) {
@@ -183,9 +211,7 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
   g.b_scale = b->scale;
   p->empty = g.rows == 0 || g.cols == 0;
   p->few = g.rows <= kFewRows;
-  // A tile's share of its operands' reads falls with its edge; 128 fills the chip where 256 would
-  // leave compute units without a tile.
-  p->tile = ceil_div(g.rows, 256) * ceil_div(g.cols, 256) >= 192 ? 256 : 128;
+  p->tile = int8_tile(g.rows, g.cols);
   // A launch has fewer than 2^32 lanes.
   if (p->few ? g.cols > (1 << 26) : ceil_div(g.rows, 128) * ceil_div(g.cols, 128) > (1 << 23))
     return refuse(err, MUON_EINVAL, "the result is too large");
@@ -244,14 +270,14 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
   p->pack = false;
   p->pack_ld = 0;
   p->parts_off = p->buf.ws_bytes = 0;
-  p->tile = 128;
+  p->tile = kTile128;
   a.splits = 1;
   a.piece = std::max(64, int32_t(round_up(a.tokens, 64)));
   if (!p->empty) {
     const int64_t tiles128 = ceil_div(a.n, 128) * ceil_div(a.k, 128), tiles256 = ceil_div(a.n, 256) * ceil_div(a.k, 256);
     if (tiles128 > (1 << 23)) return refuse(err, MUON_EINVAL, "the result is too large");
-    if (p->bf16 && tiles256 >= 192) p->tile = 256;
-    const int64_t tiles = p->tile == 256 ? tiles256 : tiles128;
+    if (p->bf16 && tiles256 >= 192) p->tile = kTile256;
+    const int64_t tiles = p->tile == kTile256 ? tiles256 : tiles128;
     // bf16 rows go to LDS 16 bytes at a time, by 32-bit offsets from the first of 64 tokens.
     constexpr int64_t kMaxStepLd = (1 << 24) - 8;
     if (p->bf16 && a.n > kMaxStepLd) return refuse(err, MUON_EINVAL, "bf16 dy has more than 2^24 - 8 columns");
@@ -262,11 +288,9 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
       a.n_read = int32_t(p->pack_ld);
       p->buf.ws_bytes = size_t(round_up(a.tokens * p->pack_ld * 2, 256));
     }
-    // Few tiles: the tokens are cut into pieces of at least 256, about two workgroups for each
-    // compute unit in all.
-    const int64_t most = std::max<int64_t>(1, a.tokens / 256), want = ceil_div(2 * kMaxUnits, tiles);
-    if (tiles < kMaxUnits && std::min(most, want) > 1) {
-      a.piece = int32_t(round_up(ceil_div(a.tokens, std::min(most, want)), 64));
+    a.splits = wgrad_splits(tiles, a);
+    if (a.splits > 1) {
+      a.piece = int32_t(round_up(ceil_div(a.tokens, a.splits), 64));
       a.splits = int32_t(ceil_div(a.tokens, a.piece));
     }
     if (a.splits > 1) {

@@ -50,7 +50,7 @@ struct IntPlan {
   IntArgs args;
   bool empty;       // no result
   bool few;         // the kernel for at most kFewRows rows
-  int tile;         // edge of a tile otherwise
+  int tile;         // LinearTile otherwise
   bool quantise;    // muon_int8_linear: a launch before makes the codes of x
   QuantPlan quant;  // with codes at the workspace's start, scales at scale_off
   size_t scale_off;

@@ -10,6 +10,10 @@ constexpr int kCodeBlock = 128;         // columns of a block scale; codes' rows
 constexpr int kFewRows = 64;              // most rows of the int8 products' kernel for few rows
 constexpr int kMaxIntSum = 131071;      // 128 * 128 * 131071 < 2^31
 
+// Result tiles of the products: 128 x 128 (4 waves, two workgroups per compute unit), 256 x 128 and
+// 256 x 256 (8 waves).
+enum LinearTile { kTile128 = 0, kTile256x128 = 1, kTile256 = 2 };
+
 struct QuantArgs {
   const void* x;
   int64_t ld;
