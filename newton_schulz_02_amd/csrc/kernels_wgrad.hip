@@ -291,12 +291,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
   wgrad_tile<T, ADD, WM, WN, FM, FN>(a);
 }
 
-// fp32 dy: 128 x 128 tiles of 4 waves, 16 tokens a step, through registers.
+// fp32 dy: 128 x 128 tiles of 4 waves, 32 tokens a step, through registers; two workgroups share a
+// compute unit, so that one multiplies while the other writes to LDS.
 template <typename T, bool ADD>
-__global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
-  constexpr int kT = 128, kTok = 16, kLd = kT + 4;
+__global__ __launch_bounds__(256, 2) void k_wgrad_f32(WgradArgs a) {
+  constexpr int kT = 128, kTok = 32, kLd = kT + 4, kUnits = kTok / 16;
   __shared__ __attribute__((aligned(16))) float lds[2][2][kTok * kLd];
-  __shared__ float parts[4 * store_floats<2>()];
+  static_assert(sizeof(lds) >= 4 * store_floats<2>() * 4, "the stages hold the waves' parts of the store pass");
   const int tm = (a.n + kT - 1) / kT, tn = (a.k + kT - 1) / kT;
   int ti, tj;
   full_band_decode(xcd_remap(int(blockIdx.x), int(gridDim.x)), tm, tn, ti, tj);
@@ -311,31 +312,40 @@ __global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = 0.0f;
 
-  const int t = tid >> 4, c = (tid & 15) * 8;  // a lane's token and first of 8 columns
-  Eight<float> dy;
-  uint2 codes = {};
-  float scale = 0.0f;
+  // A lane has 8 columns of tokens tid / 16 and tid / 16 + 16.
+  const int t = tid >> 4, c = (tid & 15) * 8;
+  const int col = min(col0 + c, a.pitch - 8), group = min(col / kCodeBlock, a.groups - 1);
+  Eight<float> dy[kUnits];
+  u32x2 codes[kUnits];
+  float scale[kUnits];
   auto load = [&](int ks) {
-    const bool there = ks * kTok + t < tokens;
-    const int64_t at = t0 + min(ks * kTok + t, tokens - 1);
-    dy.clear();
-    if (there) dy.load(static_cast<const float*>(a.dy) + at * a.lddy, row0 + c, a.n);
-    const int col = min(col0 + c, a.pitch - 8);
-    codes = *reinterpret_cast<const uint2*>(a.q + at * a.pitch + col);
-    scale = there ? a.scale[at * a.groups + min(col / kCodeBlock, a.groups - 1)] : 0.0f;
-  };
-  auto put = [&](int s) {
-    float f[8];
-    decode8(codes, scale, f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lds[s][0][t * kLd + c + e] = dy.get(e);
-      lds[s][1][t * kLd + c + e] = f[e];
+    for (int u = 0; u < kUnits; ++u) {
+      const int at = ks * kTok + t + 16 * u;
+      const int64_t row = t0 + min(at, tokens - 1);
+      dy[u].clear();
+      if (at < tokens) dy[u].load(static_cast<const float*>(a.dy) + row * a.lddy, row0 + c, a.n);
+      codes[u] = *(global_ptr<const u32x2>)(a.q + row * a.pitch + col);
+      scale[u] = *(global_ptr<const float>)(a.scale + row * a.groups + group);
+    }
+  };
+  auto put = [&](int ks) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      float f[8];
+      decode8(make_uint2(codes[u][0], codes[u][1]), ks * kTok + t + 16 * u < tokens ? scale[u] : 0.0f, f);
+      f32x4* pa = reinterpret_cast<f32x4*>(&lds[ks & 1][0][(t + 16 * u) * kLd + c]);
+      f32x4* pb = reinterpret_cast<f32x4*>(&lds[ks & 1][1][(t + 16 * u) * kLd + c]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pa[h] = f32x4{dy[u].get(4 * h), dy[u].get(4 * h + 1), dy[u].get(4 * h + 2), dy[u].get(4 * h + 3)};
+        pb[h] = f32x4{f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
+      }
     }
   };
   if (steps > 0) load(0);
   for (int ks = 0; ks < steps; ++ks) {
-    put(ks & 1);
+    put(ks);
     __syncthreads();
     if (ks + 1 < steps) load(ks + 1);
     const float* pa = lds[ks & 1][0] + lk * kLd + wm * 64 + lr;
@@ -351,6 +361,8 @@ __global__ __launch_bounds__(256, 1) void k_wgrad_f32(WgradArgs a) {
         for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
+  __syncthreads();  // the store pass uses the LDS
+  float* parts = &lds[0][0][0];
   put_block<T, ADD>(a, acc, parts + wave * store_floats<2>(), row0 + wm * 64, col0 + wn * 64);
 }
 

@@ -119,14 +119,15 @@ void set_quant(const muon_view& x, bool transpose, QuantPlan* p) {
 }
 
 // Few tiles: the tokens are cut into pieces, whose partial results a second launch joins.  In
-// microseconds: a step of 64 tokens takes 0.66 where the workgroups share no compute unit, a join
-// 3, a tenth for each piece and its bytes at 5 TB/s.
-int32_t wgrad_splits(int64_t tiles, const WgradArgs& a) {
+// microseconds: a step of 64 tokens takes 0.66 (fp32 dy: 4.5) where the workgroups share no compute
+// unit, a join 3, a tenth for each piece and its bytes at 5 TB/s.
+int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
+  const double step = bf16 ? 0.66 : 4.5;
   const double steps = double(ceil_div(a.tokens, 64)), bytes = 8.0 * a.n * a.k;
-  double best = 0.66 * steps * std::max(1.0, double(tiles) / 384);
+  double best = step * steps * std::max(1.0, double(tiles) / 384);
   int32_t splits = 1;
   for (int32_t s = 2; s <= 64 && s <= steps / 2 && tiles * s <= 3 * kMaxUnits; ++s) {
-    const double t = 0.66 * double(ceil_div(int64_t(steps), s)) * std::max(1.0, double(tiles * s) / 384) + 3.0 + 0.1 * s +
+    const double t = step * double(ceil_div(int64_t(steps), s)) * std::max(1.0, double(tiles * s) / 384) + 3.0 + 0.1 * s +
                      s * bytes / 5e6;
     if (t < best) best = t, splits = s;
   }
@@ -288,7 +289,7 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
       a.n_read = int32_t(p->pack_ld);
       p->buf.ws_bytes = size_t(round_up(a.tokens * p->pack_ld * 2, 256));
     }
-    a.splits = wgrad_splits(tiles, a);
+    a.splits = wgrad_splits(tiles, a, p->bf16);
     if (a.splits > 1) {
       a.piece = int32_t(round_up(ceil_div(a.tokens, a.splits), 64));
       a.splits = int32_t(ceil_div(a.tokens, a.piece));
