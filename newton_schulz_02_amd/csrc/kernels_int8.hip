@@ -222,24 +222,32 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
       w[u][c][1] = __builtin_nontemporal_load(p + 4);
     }
   };
+  auto load_first = [&] {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (wave + u * kFewWaves < steps) load_b(wave + u * kFewWaves, u);
-
+    for (int u = 0; u < kAhead; ++u)
+      if (wave + u * kFewWaves < steps) load_b(wave + u * kFewWaves, u);
+  };
   if constexpr (FUSED) {
-    // The waves in groups of `team`, each with one row at a time, whose first 4 chunks of 8 values a
-    // lane are kept between the maximum and the codes.
-    constexpr int kHold = 4;
-    const int team = a.rows == 1 ? 8 : a.rows == 2 ? 4 : a.rows <= 4 ? 2 : 1;
+    // The waves in groups of `team`, each with one row at a time, whose first kHold chunks of 8 values a
+    // lane are kept between the maximum and the codes.  Loads arrive in their order, so the first
+    // rows are asked for before B (behind it, the codes were begun when all of B had come).
+    constexpr int kHold = 2;
+    const int team = a.rows == 1 ? kFewWaves : a.rows == 2 ? kFewWaves / 2 : a.rows <= 4 ? kFewWaves / 4 : 1;
     const int at_once = kFewWaves / team;
-    for (int r0 = 0, turn = 0; r0 < a.rows; r0 += at_once, ++turn) {
-      const int row = r0 + wave / team;
-      const T* x = static_cast<const T*>(a.x) + int64_t(min(row, a.rows - 1)) * a.ldx;
-      const int first = (wave % team) * 64 + lane, stride = team * 64;
-      Eight<T> v[kHold];
-      typename Eight<T>::Tops tops_of;
+    const int first = (wave % team) * 64 + lane, stride = team * 64;
+    Eight<T> v[kHold];
+    auto row_of = [&](int row) { return static_cast<const T*>(a.x) + int64_t(min(row, a.rows - 1)) * a.ldx; };
+    auto load_row = [&](const T* x) {
 #pragma unroll
       for (int i = 0; i < kHold; ++i) v[i].load(x, (first + i * stride) * 8, a.k);
+    };
+    load_row(row_of(wave / team));
+    load_first();
+    for (int r0 = 0, turn = 0; r0 < a.rows; r0 += at_once, ++turn) {
+      const int row = r0 + wave / team;
+      const T* x = row_of(row);
+      if (r0 > 0) load_row(x);
+      typename Eight<T>::Tops tops_of;
 #pragma unroll
       for (int i = 0; i < kHold; ++i) tops_of.take(v[i]);
       for (int c = first + kHold * stride; c * 8 < a.pitch; c += stride) {
@@ -270,6 +278,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
       }
     }
     __syncthreads();
+  } else {
+    load_first();
   }
   const char* rows = FUSED ? codes : reinterpret_cast<const char*>(a.a);
   int at[G];  // few rows: 64 * 131072 bytes at most

@@ -222,9 +222,12 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
     g.x_bf16 = x->dtype == MUON_BF16;
     g.ldx = rows > 1 ? x->ld : x->cols;
     g.x = x->data;
-    // Codes made inside the product save a launch (3 us of the host's time), but every workgroup
-    // reads x again: up to 4 rows, or 16 KB of codes.
-    p->quantise = !p->empty && !((g.rows <= 4 && g.rows * g.pitch <= 48 * 1024) || (g.rows <= 16 && g.rows * g.pitch <= 16 * 1024));
+    // Codes made inside the product save a launch (3 us of the host's time), but each of its
+    // workgroups of 16 columns reads x: 1 or 2 rows, or 4 MB in all (4 rows of 4096 for 11008 columns,
+    // 11 MB, take 18 us that way and 16 in two launches).
+    const int64_t codes = int64_t(g.rows) * g.pitch;
+    const bool fused = g.rows <= 16 && codes <= 48 * 1024 && (g.rows <= 2 || ceil_div(g.cols, 16) * codes <= (4 << 20));
+    p->quantise = !p->empty && !fused;
     g.fused = !p->quantise;
     if (p->quantise) {
       set_quant(*x, false, &p->quant);
