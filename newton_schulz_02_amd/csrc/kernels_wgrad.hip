@@ -44,10 +44,11 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// A wave's block of results, from row wrow and column wcol on: to the output (T), added to what is
-// there with ADD, or to a piece's partial results.
+// A wave's block of results, from row wrow and column wcol on, less the rows before row_lo: to the
+// output (T), added to what is there with ADD, or to a piece's partial results.
 template <typename T, bool ADD, int FM, int FN>
-__device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc)[FM][FN], float* part, int wrow, int wcol) {
+__device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc)[FM][FN], float* part, int wrow, int wcol,
+                                          int row_lo) {
   constexpr int E = Run<T>::E;
   const bool pieces = a.splits > 1;  // T is float then
   T* out = pieces ? reinterpret_cast<T*>(a.parts) + int64_t(blockIdx.y) * a.n * a.k : static_cast<T*>(a.out);
@@ -60,11 +61,12 @@ __device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc
         [&](int r) {
           Run<T> old;
           old.v = 0;
-          if (ADD && (kWhole || (wrow + r < a.n && col < a.k))) old.template load<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
+          if (ADD && (kWhole || (wrow + r >= row_lo && wrow + r < a.n && col < a.k)))
+            old.template load<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
           return old;
         },
         [&](int r, const float (&v)[E], const Run<T>& old) {
-          if (!kWhole && (wrow + r >= a.n || col >= a.k)) return;
+          if (!kWhole && (wrow + r < row_lo || wrow + r >= a.n || col >= a.k)) return;
           float f[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) f[e] = ADD ? old.get(e) + v[e] : v[e];
@@ -73,7 +75,7 @@ __device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc
           x.template store<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
         });
   };
-  if (wrow + FM * 32 <= a.n && wcol + FN * 32 <= a.k) store(std::true_type{});
+  if (wrow >= row_lo && wrow + FM * 32 <= a.n && wcol + FN * 32 <= a.k) store(std::true_type{});
   else store(std::false_type{});
 }
 
@@ -88,7 +90,11 @@ __device__ __forceinline__ int place(int c, int t) { return c ^ (((t & 3) << 2) 
 // LDS and the codes of step ks + 2 to registers; those of step ks + 1, in registers, are decoded
 // into x's other stage between the matrix instructions.  Each stage is an array of its own, so
 // that the compiler does not take the writes of one for the loads of another.
-template <typename T, bool ADD, int WM, int WN, int FM, int FN>
+//
+// THROUGH: dy's rows are not 16-byte aligned, which loads to LDS have to be, and come through
+// registers, written to LDS a step after they were asked for.  The last tile begins early enough to
+// be whole (n is at least a tile then), and leaves the rows that it shares to the tile before.
+template <typename T, bool ADD, bool THROUGH, int WM, int WN, int FM, int FN>
 __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   constexpr int kWaves = WM * WN, kThreads = kWaves * 64, kTM = WM * FM * 32, kTN = WN * FN * 32;
   constexpr int kRowA = kTM * 2, kRowB = kTN * 2;  // bytes of a token's row in LDS
@@ -113,7 +119,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   const int tm = (a.n + kTM - 1) / kTM, tn = (a.k + kTN - 1) / kTN;
   int ti, tj;
   full_band_decode(xcd_remap(int(blockIdx.x), int(gridDim.x)), tm, tn, ti, tj);
-  const int row0 = ti * kTM, col0 = tj * kTN;
+  const int row_lo = ti * kTM, row0 = THROUGH ? min(row_lo, a.n - kTM) : row_lo, col0 = tj * kTN;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WN, wn = wave % WN;
   const int t0 = int(blockIdx.y) * a.piece, tokens = min(a.piece, a.tokens - t0);
@@ -138,8 +144,13 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
     tok[j] = (wave * kInstA + j) * kRowsInst + lane / kChunksA;
     src[j] = min(row0 + place(lane % kChunksA, tok[j]) * 8, a.n_read - 8) * 2;
   }
+  u32x4 through[THROUGH ? kInstA : 1] = {};
   auto load_dy = [&](int ks, int j, char* st) {
     const int first = min(ks * kStep, tokens - 1), left = tokens - 1 - first;
+    if constexpr (THROUGH) {
+      through[j] = *(global_ptr<const u32x4_at2>)(dy + int64_t(first) * ld2 + uint32_t(min(tok[j], left) * ld2 + src[j]));
+      return;
+    }
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<char*>(dy + int64_t(first) * ld2), (short)0, min(left, kStep - 1) * ld2 + a.n_read * 2, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(st + (wave * kInstA + j) * 1024), 16,
@@ -164,10 +175,14 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   };
   // The share of a step's loads that goes with fragment group kk.  A wave's loads of 1 KB each keep
   // the address unit busy for 16 cycles: together at the step's start, they held all waves up.
-  auto load_share = [&](int ks, int kk, char* st, auto set) {
+  auto load_share = [&](int ks, int kk, char* st, auto set, char* before) {
 #pragma unroll
     for (int j = 0; j < kInstA; ++j)
-      if (j * kGroups / kInstA == kk) load_dy(ks, j, st);
+      if (j * kGroups / kInstA == kk) {
+        // What step ks - 1 will read.
+        if constexpr (THROUGH) *reinterpret_cast<u32x4*>(before + (wave * kInstA + j) * 1024 + lane * 16) = through[j];
+        load_dy(ks, j, st);
+      }
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
       if (u * kGroups / kUnits == kk) load_x(ks, set, u);
@@ -213,10 +228,12 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
 
   // Loads are counted in their order: when step ks begins, behind dy of step ks there are codes of
   // step ks (used already), and dy and the codes of step ks + 1 in flight: kInstA loads and 2 a
-  // unit (the barrier's empty asm statements keep a step's loads in it).  The last steps, too, load and decode what would come next (the last token, and nothing reads it): without
-  // branches the compiler mixes a step's parts, and keeps the results where they are.
-  auto step = [&](int ks, char* sa, char* sb, char* next_a, char* next_b, auto set, auto other) {
-    wait_vm<kInstA + 2 * kUnits>();
+  // unit (the barrier's empty asm statements keep a step's loads in it).  The last steps, too, load
+  // and decode what would come next (the last token, and nothing reads it): without branches the
+  // compiler mixes a step's parts, and keeps the results where they are.  next_a, next_b: where dy
+  // of step ks + 2 and x of step ks + 1 go; mid_a: dy of step ks + 1.
+  auto step = [&](int ks, char* sa, char* sb, char* mid_a, char* next_a, char* next_b, auto set, auto other) {
+    if constexpr (!THROUGH) wait_vm<kInstA + 2 * kUnits>();
     wait_lds();
     stage_barrier();  // all waves' dy and codes of this step are there, and what step ks - 1 read is free
     if (tokens - ks * kStep < kStep) {
@@ -232,7 +249,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
     static_for<kGroups>([&](auto kc) {
       constexpr int kk = decltype(kc)::value, cur = kk & 1;
       constexpr bool kNext = kk + 1 < kGroups;
-      load_share(ks + 2, kk, next_a, set);
+      load_share(ks + 2, kk, next_a, set, mid_a);
       if constexpr (kNext) load_frags(sa, sb, kk + 1, fa[cur ^ 1], fb[cur ^ 1]);
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -248,7 +265,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
         if constexpr (kNext) __builtin_amdgcn_sched_group_barrier(0x100, (2 * (FM + FN) + FM * FN - 1) / (FM * FN), 0);
         __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
       });
-      __builtin_amdgcn_sched_group_barrier(0x200, kPieces, 0);
+      __builtin_amdgcn_sched_group_barrier(0x200, kPieces + (THROUGH ? kInstA / kGroups : 0), 0);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -256,24 +273,24 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
     constexpr std::integral_constant<int, 0> x0{};
     constexpr std::integral_constant<int, 1> x1{};
 #pragma unroll
-    for (int kk = 0; kk < kGroups; ++kk) load_share(0, kk, a0, x0);
+    for (int kk = 0; kk < kGroups; ++kk) load_share(0, kk, a0, x0, a2);
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int p = 0; p < 2 * kUnits; ++p) put_x(0, x0, p >> 1, p & 1, b0);
 #pragma unroll
-    for (int kk = 0; kk < kGroups; ++kk) load_share(1, kk, a1, x1);
+    for (int kk = 0; kk < kGroups; ++kk) load_share(1, kk, a1, x1, a0);
     for (int ks = 0;; ks += 6) {
-      step(ks, a0, b0, a2, b1, x0, x1);
+      step(ks, a0, b0, a1, a2, b1, x0, x1);
       if (ks + 1 >= steps) break;
-      step(ks + 1, a1, b1, a0, b0, x1, x0);
+      step(ks + 1, a1, b1, a2, a0, b0, x1, x0);
       if (ks + 2 >= steps) break;
-      step(ks + 2, a2, b0, a1, b1, x0, x1);
+      step(ks + 2, a2, b0, a0, a1, b1, x0, x1);
       if (ks + 3 >= steps) break;
-      step(ks + 3, a0, b1, a2, b0, x1, x0);
+      step(ks + 3, a0, b1, a1, a2, b0, x1, x0);
       if (ks + 4 >= steps) break;
-      step(ks + 4, a1, b0, a0, b1, x0, x1);
+      step(ks + 4, a1, b0, a2, a0, b1, x0, x1);
       if (ks + 5 >= steps) break;
-      step(ks + 5, a2, b1, a1, b0, x1, x0);
+      step(ks + 5, a2, b1, a0, a1, b0, x1, x0);
       if (ks + 6 >= steps) break;
     }
     wait_vm<0>();  // what the last step loaded
@@ -283,12 +300,12 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
   const int array = wave / kPartWaves;
   char* base = array == 0 ? a0 : array == 1 ? a1 : array == 2 ? b0 : b1;
   put_block<T, ADD>(a, acc, reinterpret_cast<float*>(base + wave % kPartWaves * kPart), row0 + wm * FM * 32,
-                    col0 + wn * FN * 32);
+                    col0 + wn * FN * 32, row_lo);
 }
 
-template <typename T, bool ADD, int WM, int WN, int FM, int FN>
+template <typename T, bool ADD, bool THROUGH, int WM, int WN, int FM, int FN>
 __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
-  wgrad_tile<T, ADD, WM, WN, FM, FN>(a);
+  wgrad_tile<T, ADD, THROUGH, WM, WN, FM, FN>(a);
 }
 
 // fp32 dy: 128 x 128 tiles of 4 waves, 32 tokens a step, through registers; two workgroups share a
@@ -363,7 +380,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad_f32(WgradArgs a) {
   }
   __syncthreads();  // the store pass uses the LDS
   float* parts = &lds[0][0][0];
-  put_block<T, ADD>(a, acc, parts + wave * store_floats<2>(), row0 + wm * 64, col0 + wn * 64);
+  put_block<T, ADD>(a, acc, parts + wave * store_floats<2>(), row0 + wm * 64, col0 + wn * 64, row0);
 }
 
 // Partial results of the pieces, in their order, to the output.
@@ -402,8 +419,9 @@ void launch(const WgradArgs& a, bool dy_bf16, int tile, hipStream_t s) {
   const int64_t tiles = int64_t((a.n + edge - 1) / edge) * ((a.k + edge - 1) / edge);
   const dim3 grid(uint32_t(tiles), uint32_t(a.splits));
   if (!dy_bf16) hipLaunchKernelGGL((k_wgrad_f32<T, ADD>), grid, dim3(256), 0, s, a);
-  else if (tile == kTile256) hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((k_wgrad<T, ADD, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+  else if (tile == kTile256) hipLaunchKernelGGL((k_wgrad<T, ADD, false, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+  else if (a.through) hipLaunchKernelGGL((k_wgrad<T, ADD, true, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_wgrad<T, ADD, false, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <typename T, bool ADD>

@@ -282,12 +282,17 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
     if (tiles128 > (1 << 23)) return refuse(err, MUON_EINVAL, "the result is too large");
     if (p->bf16 && tiles256 >= 192) p->tile = kTile256;
     const int64_t tiles = p->tile == kTile256 ? tiles256 : tiles128;
-    // bf16 rows go to LDS 16 bytes at a time, by 32-bit offsets from the first of 64 tokens.
+    // bf16 rows go to LDS 16 bytes at a time, by 32-bit offsets from the first of 64 tokens.  Others
+    // come through registers, in small tiles, or are copied first (517 x 1031 from 777 tokens: 15 us
+    // through registers, 20 with the copy).
     constexpr int64_t kMaxStepLd = (1 << 24) - 8;
     if (p->bf16 && a.n > kMaxStepLd) return refuse(err, MUON_EINVAL, "bf16 dy has more than 2^24 - 8 columns");
     if (p->bf16 && a.tokens > 0 &&
         (reinterpret_cast<uintptr_t>(dy->data) % 16 || a.lddy % 8 || a.n % 8 || a.lddy > kMaxStepLd)) {
-      p->pack = true;
+      a.through = p->tile == kTile128 && a.n >= 128 && a.lddy <= kMaxStepLd;
+      p->pack = !a.through;
+    }
+    if (p->pack) {
       p->pack_ld = round_up(a.n, 8);
       a.n_read = int32_t(p->pack_ld);
       p->buf.ws_bytes = size_t(round_up(a.tokens * p->pack_ld * 2, 256));

@@ -65,6 +65,7 @@ struct WgradArgs {
   int32_t tokens;
   int32_t n, k;
   int32_t n_read;        // bf16: columns of dy that can be read, a multiple of 8
+  int32_t through;       // bf16, 128 x 128 tiles: dy's rows are not 16-byte aligned
   int32_t pitch, groups;
   int32_t splits;        // pieces of the tokens
   int32_t piece;         // tokens of a piece (a multiple of 64)
