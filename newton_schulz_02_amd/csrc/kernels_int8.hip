@@ -170,7 +170,7 @@ __device__ __forceinline__ void int8_tile(const IntArgs& a) {
   for (int e = 0; e < E; ++e) sb[e] = *(global_ptr<const float>)(a.b_scale + min(col + e, a.cols - 1));
   auto store = [&](auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
-    store_block<FM, FN, E>(
+    store_block<FM, FN, E, !kWhole>(
         acc, part,
         [&](int r) { return *(global_ptr<const float>)(a.a_scale + (kWhole ? wrow + r : min(wrow + r, a.rows - 1))); },
         [&](int r, const float (&v)[E], float sa) {

@@ -56,17 +56,18 @@ __device__ __forceinline__ void put_block(const WgradArgs& a, const f32x16 (&acc
   const int col = wcol + store_col<FN, E>();
   auto store = [&](auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
-    store_block<FM, FN, E>(
+    store_block<FM, FN, E, !kWhole>(
         acc, part,
         [&](int r) {
           Run<T> old;
           old.v = 0;
-          if (ADD && (kWhole || (wrow + r >= row_lo && wrow + r < a.n && col < a.k)))
-            old.template load<kWhole>(out + int64_t(wrow + r) * ld, col, a.k);
+          if (ADD && kWhole) old.load(out + int64_t(wrow + r) * ld + col);
+          else if (ADD) old.load_edge(out + int64_t(min(wrow + r, a.n - 1)) * ld, min(col, a.k - 1), a.k);
           return old;
         },
-        [&](int r, const float (&v)[E], const Run<T>& old) {
+        [&](int r, const float (&v)[E], Run<T> old) {
           if (!kWhole && (wrow + r < row_lo || wrow + r >= a.n || col >= a.k)) return;
+          if (ADD && !kWhole) old.settle(col, a.k);
           float f[E];
 #pragma unroll
           for (int e = 0; e < E; ++e) f[e] = ADD ? old.get(e) + v[e] : v[e];

@@ -36,10 +36,13 @@ struct Eight<uint16_t> {
     clear();
     if (at + 8 <= cols) {
       v = *(global_ptr<const u32x4_at2>)(row + at);
-    } else {
+    } else if (at < cols) {
+      // All loads at once, without a branch for each.
+      uint16_t x[7];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < cols) v[e / 2] |= uint32_t(*(global_ptr<const uint16_t>)(row + at + e)) << (16 * (e & 1));
+      for (int e = 0; e < 7; ++e) x[e] = *(global_ptr<const uint16_t>)(row + min(at + e, cols - 1));
+#pragma unroll
+      for (int e = 0; e < 7; ++e) v[e / 2] |= (at + e < cols ? uint32_t(x[e]) : 0u) << (16 * (e & 1));
     }
   }
   __device__ __forceinline__ float get(int e) const { return __uint_as_float(e & 1 ? v[e / 2] & 0xffff0000u : v[e / 2] << 16); }
@@ -84,10 +87,12 @@ struct Eight<float> {
     if (at + 8 <= cols) {
       const global_ptr<const u32x4_at4> p = (global_ptr<const u32x4_at4>)(row + at);
       v[0] = p[0], v[1] = p[1];
-    } else {
+    } else if (at < cols) {
+      float x[7];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < cols) v[e / 4][e % 4] = __float_as_uint(*(global_ptr<const float>)(row + at + e));
+      for (int e = 0; e < 7; ++e) x[e] = *(global_ptr<const float>)(row + min(at + e, cols - 1));
+#pragma unroll
+      for (int e = 0; e < 7; ++e) v[e / 4][e % 4] = at + e < cols ? __float_as_uint(x[e]) : 0u;
     }
   }
   __device__ __forceinline__ float get(int e) const { return __uint_as_float(v[e / 4][e % 4]); }

@@ -44,33 +44,46 @@ struct Run {
       else v[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
     }
   }
-  // Whole, at any alignment of T, or the values before column `cols`.
+  // At any alignment of T.  Non-temporal as the stores, but not for bf16, where a run is half of what
+  // the lane beside it will ask for again (an fp32 gradient of 4096 x 4096 added to: 33.4 -> 30.0
+  // us for 128 tokens; a bf16 one 16.5 -> 17.9).
   using At = typename std::conditional<sizeof(T) == 4, u32x4_at4, u32x4_at2>::type;
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(const T* row, int col, int cols) {
-    if constexpr (WHOLE) {
-      // Non-temporal as the stores, but not for bf16, where a run is half of what the lane beside it
-      // will ask for again (an fp32 gradient of 4096 x 4096 added to: 33.4 -> 30.0 us for 128
-      // tokens; a bf16 one 16.5 -> 17.9).
-      if constexpr (sizeof(T) == 4) v = __builtin_nontemporal_load((global_ptr<const At>)(row + col));
-      else v = *(global_ptr<const At>)(row + col);
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(T) == 4) v = __builtin_nontemporal_load((global_ptr<const At>)(p));
+    else v = *(global_ptr<const At>)(p);
+  }
+  // A run of a row of `cols` values that may end before it.  Of a row of E values or more the load
+  // is one access, that of the row's last E values where the run passes the end, and `settle` moves
+  // them into place when they are used: no branch, so that loads are not waited for one by one.
+  __device__ __forceinline__ void load_edge(const T* row, int col, int cols) {
+    if (cols >= E) {
+      load(row + min(col, cols - E));
     } else {
       v = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
+      for (int e = 0; e < E - 1; ++e)
         if (col + e < cols) {
           if constexpr (sizeof(T) == 4) v[e] = *(global_ptr<const uint32_t>)(row + col + e);
           else v[e / 2] |= uint32_t(*(global_ptr<const uint16_t>)(row + col + e)) << (16 * (e & 1));
         }
     }
   }
+  __device__ __forceinline__ void settle(int col, int cols) {
+    int by = cols >= E ? max(0, col + E - cols) : 0;  // values to move down
+    if constexpr (sizeof(T) == 2) {
+      if (by & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+      by >>= 1;
+    }
+    if (by & 1) v = u32x4{v[1], v[2], v[3], 0};
+    if (by & 2) v = u32x4{v[2], v[3], 0, 0};
+  }
   template <bool WHOLE>
   __device__ __forceinline__ void store(T* row, int col, int cols) const {
-    if constexpr (WHOLE) {
+    if (WHOLE || col + E <= cols) {
       __builtin_nontemporal_store(v, (global_ptr<At>)(row + col));
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
+      for (int e = 0; e < E - 1; ++e)
         if (col + e < cols) {
           if constexpr (sizeof(T) == 4) *(global_ptr<uint32_t>)(row + col + e) = v[e];
           else *(global_ptr<uint16_t>)(row + col + e) = uint16_t(v[e / 2] >> (16 * (e & 1)));
@@ -93,8 +106,10 @@ __device__ __forceinline__ int store_col() {
 }
 
 // For every run of a wave's block: put(row, its E accumulators, fetch(row)), with the row within the
-// block; the fetches of 32 rows are in flight while the 32 before are put.
-template <int FM, int FN, int E, typename V, typename Fetch, typename Put>
+// block; the fetches of 32 rows are in flight while the 32 before are put.  DRAIN: put has branches,
+// behind which the compiler no longer knows which loads are done and waits for all accesses, the
+// stores among them, at every run; the loads are waited for once, before the stores, instead.
+template <int FM, int FN, int E, bool DRAIN, typename V, typename Fetch, typename Put>
 __device__ __forceinline__ void store_block(const V (&acc)[FM][FN], float* part, Fetch&& fetch, Put&& put) {
   constexpr int kLd = FN * 32 + 4, kRuns = FN * 32 / E, kU = 32 * kRuns / 64, kRows = 64 / kRuns;
   const int lane = threadIdx.x & 63, lr = lane & 31, lk = lane >> 5;
@@ -120,6 +135,7 @@ __device__ __forceinline__ void store_block(const V (&acc)[FM][FN], float* part,
         }
         *reinterpret_cast<f32x4*>(part + lr * kLd + 32 * j + 8 * g + 4 * lk) = v;
       }
+    if constexpr (DRAIN) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
