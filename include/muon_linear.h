@@ -70,9 +70,10 @@ typedef struct muon_codes {
   int32_t reserved; /* must be 0 */
 } muon_codes;
 
-/* The sizes below: rows and cols from 0 to 2^31 - 1 (muon_int8_matmul and muon_int8_linear: at
- * most 131071 columns are summed over).  `workspace` is device memory of at least the size that
- * the call's _size function gives (0: NULL will do), 256-byte aligned, owned by the caller and
+/* Sizes: rows and cols from 0 to 2^30; muon_int8_matmul and muon_int8_linear sum over at most 131071
+ * columns; muon_weight_grad of a bf16 dy takes at most 2^24 - 8 columns of dy and of x; and results
+ * of more than 2^23 tiles of 128 x 128 (2^26 columns for up to 64 rows) are refused.  `workspace` is device memory of at least the size that
+ * the call's _size function gives for the same arguments (0: NULL will do), 256-byte aligned, owned by the caller and
  * written by nothing else until the stream has passed the call; its contents do not matter, and
  * calls in flight at once need one each.  An output may overlap no input, no other output and
  * not the workspace (MUON_EALIAS); interleaved rows of one wider buffer do not overlap. */

@@ -118,6 +118,11 @@ void set_quant(const muon_view& x, bool transpose, QuantPlan* p) {
   }
 }
 
+// A launch has fewer than 2^32 lanes.
+bool quant_too_large(const QuantPlan& p) {
+  return p.transpose && ceil_div(p.args.rows, 128) * (p.args.pitch / 128) > (1 << 23);
+}
+
 // Few tiles: the tokens are cut into pieces, whose partial results a second launch joins.  In
 // microseconds: a step of 64 tokens takes 0.66 (fp32 dy: 4.5) where the workgroups share no compute
 // unit, a join 3, a tenth for each piece and its bytes at 5 TB/s.
@@ -155,6 +160,7 @@ int plan_quantize(const muon_view* x, int32_t transpose, const muon_codes* codes
   if (rc != MUON_OK) return rc;
   if (transpose != 0 && transpose != 1) return refuse(err, MUON_EINVAL, "transpose must be 0 or 1");
   set_quant(*x, transpose != 0, p);
+  if (quant_too_large(*p)) return refuse(err, MUON_EINVAL, "x is too large for codes of its columns");
   if (!codes) return MUON_OK;
   if ((rc = check_codes("codes", codes, transpose ? 0 : -1, &q, &scale, err)) != MUON_OK) return rc;
   if (codes->rows != p->args.rows || codes->cols != p->args.cols)
@@ -213,7 +219,6 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
   p->empty = g.rows == 0 || g.cols == 0;
   p->few = g.rows <= kFewRows;
   p->tile = int8_tile(g.rows, g.cols);
-  // A launch has fewer than 2^32 lanes.
   if (p->few ? g.cols > (1 << 26) : ceil_div(g.rows, 128) * ceil_div(g.cols, 128) > (1 << 23))
     return refuse(err, MUON_EINVAL, "the result is too large");
   p->quantise = false;
@@ -286,7 +291,8 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
     // come through registers, in small tiles, or are copied first (517 x 1031 from 777 tokens: 15 us
     // through registers, 20 with the copy).
     constexpr int64_t kMaxStepLd = (1 << 24) - 8;
-    if (p->bf16 && a.n > kMaxStepLd) return refuse(err, MUON_EINVAL, "bf16 dy has more than 2^24 - 8 columns");
+    if (p->bf16 && (a.n > kMaxStepLd || a.k > kMaxStepLd))
+      return refuse(err, MUON_EINVAL, "more than 2^24 - 8 columns of bf16 dy or of x");
     if (p->bf16 && a.tokens > 0 &&
         (reinterpret_cast<uintptr_t>(dy->data) % 16 || a.lddy % 8 || a.n % 8 || a.lddy > kMaxStepLd)) {
       a.through = p->tile == kTile128 && a.n >= 128 && a.lddy <= kMaxStepLd;

@@ -482,3 +482,43 @@ def test_profile_names_the_launches():
     stats = nm.profile_end()
     for name in ("quantize_rows", "quantize_blocks", "quantize_columns", "dequantize", "int8_product", "int8_few", "weight_grad"):
         assert stats[name]["launches"] >= 1
+
+
+def test_more_than_2_31_elements():
+    """The last rows of operands and results behind 2^31 elements are those of a call on them alone."""
+    rows, cols = 70003, 32776
+    x = torch.empty(rows, cols, device=DEV, dtype=BF16).normal_(generator=gen(1))
+    tail = x[-200:]
+    c, kept = nm.quantize(x), nm.quantize(x, block=True)
+    for got, block in ((c, False), (kept, True)):
+        part = nm.quantize(tail, block=block)
+        assert torch.equal(got.q[-200:], part.q) and torch.equal(got.scale[-200:], part.scale)
+        del part
+    w = nm.quantize(normal(40, cols, BF16, 2))
+    assert torch.equal(nm.int8_matmul(c, w)[-200:], nm.int8_matmul(nm.quantize(tail), w))
+    few = nm.quantize(normal(3, cols, BF16, 3))
+    assert torch.equal(nm.int8_matmul(few, c)[:, -200:], nm.int8_matmul(few, nm.quantize(tail)))
+    # Only the last 200 tokens' dy is not zero; whole numbers, so that sums are exact in any order.
+    x[-200:] = whole(200, cols, 7, BF16, 4)
+    kept = nm.quantize(x, block=True)
+    values = kept.dequantize()
+    assert torch.equal(values[-200:], tail)
+    dy = torch.zeros(rows, 24, device=DEV, dtype=BF16)
+    dy[-200:] = whole(200, 24, 7, BF16, 5)
+    want = nm.weight_grad(dy[-200:], nm.quantize(tail, block=True))
+    assert torch.equal(nm.weight_grad(dy, kept), want)
+    assert torch.equal(nm.weight_grad(dy.float(), kept), want)
+
+
+def test_results_behind_2_31_elements():
+    a, b = nm.quantize(normal(70001, 130, BF16, 1)), nm.quantize(normal(32771, 130, BF16, 2))
+    y = nm.int8_matmul(a, b)
+    assert torch.equal(y[-130:], nm.int8_matmul(nm.quantize(normal(70001, 130, BF16, 1)[-130:]), b))
+    del y, a, b
+    dy, x = whole(66, 70008, 3, BF16, 1), whole(66, 32771, 3, BF16, 2)
+    kept = nm.quantize(x, block=True)
+    dw = nm.weight_grad(dy, kept, BF16)
+    assert torch.equal(dw[-9:], (dy[:, -9:].double().t().contiguous() @ x.double()).to(BF16))
+    del dw
+    t = nm.quantize(whole(40000, 54001, 7, BF16, 3), transpose=True)
+    assert torch.equal(t.q[-70:, :40000].t(), nm.quantize(whole(40000, 54001, 7, BF16, 3)[:, -70:], transpose=True).q[:, :40000].t())

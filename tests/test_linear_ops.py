@@ -125,6 +125,9 @@ OUT = BASE + 4 * FAR
     (lambda: wgrad(view(64, 16), codes(64, 8, block=128), view(16, 8, at=OUT), 2), nm.MUON_EINVAL),
     (lambda: wgrad(view(64, 16), codes(64, 8, block=128), view(16, 8)), nm.MUON_EALIAS),
     (lambda: wgrad(view(64, 16), codes(64, 8, block=128), view(16, 8, at=BASE + FAR)), nm.MUON_EALIAS),
+    (lambda: wgrad(view(1, 1 << 24), codes(1, 8, block=128), view(1 << 24, 8, at=OUT)), nm.MUON_EINVAL),
+    (lambda: wgrad(view(1, 8), codes(1, 1 << 24, block=128), view(8, 1 << 24, at=OUT)), nm.MUON_EINVAL),
+    (lambda: quantize(view(1 << 20, 1 << 19), codes(1 << 19, 1 << 20, at=1 << 44), 1, size=1 << 45), nm.MUON_EINVAL),
     (lambda: wgrad(view(64, 15), codes(64, 8, block=128), view(15, 8, at=OUT), ws=None), nm.MUON_EINVAL),
     (lambda: wgrad(view(64, 15), codes(64, 8, block=128), view(15, 8, at=OUT), size=64 * 16 * 2 - 1), nm.MUON_ENOSPC),
     (lambda: wgrad(view(64, 15), codes(64, 8, block=128), view(15, 8, at=OUT), ws=ctypes.c_void_p(BASE)), nm.MUON_EALIAS),
