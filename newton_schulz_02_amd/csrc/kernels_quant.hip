@@ -140,17 +140,16 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
   __shared__ uint32_t tile[128 * 33];
   __shared__ uint32_t tops[2][128];
+  __shared__ float inverses[128];
   const int cols = int(a.rows), rows = a.cols;  // of x
   const int across = (cols + 127) / 128;
   const int c0 = int(blockIdx.x) % across * 128, r0 = int(blockIdx.x) / across * 128;
-  {
-    const int c = threadIdx.x & 127, half = threadIdx.x >> 7;
-    uint32_t t = 0;
-    if (c0 + c < cols)
-      for (int s = half; s < a.part_rows; s += 2) t = max(t, __float_as_uint(a.parts[int64_t(s) * cols + c0 + c]));
-    tops[half][c] = t;
-  }
   const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4;
+  const int mine = threadIdx.x & 127, half = threadIdx.x >> 7;
+  uint32_t t[kMaxStrips / 2];  // half of the strips' maxima of one column, all asked for at once
+#pragma unroll
+  for (int s = 0; s < kMaxStrips / 2; ++s)
+    t[s] = __float_as_uint(a.parts[int64_t(min(2 * s + half, a.part_rows - 1)) * cols + min(c0 + mine, cols - 1)]);
   Eight<T> v[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
@@ -158,18 +157,27 @@ __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
     v[u].clear();
     if (r < rows) v[u].load(static_cast<const T*>(a.x) + int64_t(r) * a.ld, c0 + lane * 8, cols);
   }
+#pragma unroll
+  for (int s = 1; s < kMaxStrips / 2; ++s) t[0] = max(t[0], t[s]);
+  tops[half][mine] = t[0];
+  __syncthreads();
+  // One division a column, not one for each lane that has it.
+  if (threadIdx.x < 128) {
+    const RowCoder code(max(tops[0][mine], tops[1][mine]));
+    inverses[mine] = code.inverse;
+    if (r0 == 0 && c0 + mine < cols) a.scale[c0 + mine] = code.scale();
+  }
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const RowCoder code(max(tops[0][lane * 8 + e], tops[1][lane * 8 + e]));
+    const int c = lane * 8 + e;
+    const RowCoder code(max(tops[0][c], tops[1][c]), inverses[c]);
     uint32_t w[2];
     code.codes<8>(w, [&](int u) { return v[u].get(e); });
-    tile[(lane * 8 + e) * 33 + sub] = w[0];
-    tile[(lane * 8 + e) * 33 + 16 + sub] = w[1];
+    tile[c * 33 + sub] = w[0];
+    tile[c * 33 + 16 + sub] = w[1];
   }
   __syncthreads();
-  if (r0 == 0 && threadIdx.x < 128 && c0 + int(threadIdx.x) < cols)
-    a.scale[c0 + threadIdx.x] = RowCoder(max(tops[0][threadIdx.x], tops[1][threadIdx.x])).scale();
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = u * 32 + int(threadIdx.x) / 8, part = int(threadIdx.x) & 7;

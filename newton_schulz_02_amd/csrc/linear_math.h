@@ -148,11 +148,14 @@ struct RowCoder {
   float size, inverse;
   bool lost;  // a NaN or an infinity
   bool tiny;  // scaled by 2^100 first, so that 127 / max stays finite
-  __device__ __forceinline__ explicit RowCoder(uint32_t top) {
+  __device__ __forceinline__ explicit RowCoder(uint32_t top) : RowCoder(top, 0.0f) {
+    inverse = size > 0.0f ? 127.0f / (tiny ? size * 0x1p100f : size) : 0.0f;
+  }
+  // Of another coder's maximum and `inverse`.
+  __device__ __forceinline__ RowCoder(uint32_t top, float inv) : inverse(inv) {
     lost = top >= 0x7f800000u;
     size = lost ? 0.0f : __uint_as_float(top);
     tiny = size < 0x1p-100f;
-    inverse = size > 0.0f ? 127.0f / (tiny ? size * 0x1p100f : size) : 0.0f;
   }
   __device__ __forceinline__ float scale() const { return lost ? __uint_as_float(0x7fc00000u) : size / 127.0f; }
   __device__ __forceinline__ uint32_t exact(float x) const {

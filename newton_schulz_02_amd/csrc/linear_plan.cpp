@@ -110,10 +110,10 @@ void set_quant(const muon_view& x, bool transpose, QuantPlan* p) {
   p->buf.count = 0;
   p->empty = a.rows == 0;
   if (transpose && a.rows > 0 && a.cols > 0) {
-    // Strips of at least 64 rows of x, about 1024 workgroups of 256 columns, and at most 32 strips,
+    // Strips of at least 64 rows of x, about 1024 workgroups of 256 columns, and at most kMaxStrips,
     // whose maxima the second launch reads again for each of its tiles.
     const int64_t across = ceil_div(a.rows, 256);
-    a.part_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>({ceil_div(a.cols, 64), ceil_div(1024, across), 32})));
+    a.part_rows = int32_t(std::max<int64_t>(1, std::min<int64_t>({ceil_div(a.cols, 64), ceil_div(1024, across), kMaxStrips})));
     p->buf.ws_bytes = size_t(a.rows) * size_t(a.part_rows) * 4;
   }
 }

@@ -8,6 +8,7 @@ namespace muon {
 
 constexpr int kCodeBlock = 128;         // columns of a block scale; codes' rows are padded to it
 constexpr int kFewRows = 64;              // most rows of the int8 products' kernel for few rows
+constexpr int kMaxStrips = 32;            // row strips of the columns' maxima
 constexpr int kMaxIntSum = 131071;      // 128 * 128 * 131071 < 2^31
 
 // Result tiles of the products: 128 x 128 (4 waves, two workgroups per compute unit), 256 x 128 and
