@@ -53,11 +53,15 @@ int check_size(const char* name, int64_t rows, int64_t cols, std::string* err) {
   return MUON_OK;
 }
 
-int check_pointer(const char* name, const void* p, uintptr_t align, int64_t bytes, std::string* err) {
+// `rows` runs (at least one) of `run` bytes, `step` bytes from one to the next.
+int check_pointer(const char* name, const void* p, uintptr_t align, int64_t rows, int64_t run, int64_t step, std::string* err) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
   if (!at) return refuse(err, MUON_EINVAL, std::string(name) + ": NULL pointer");
   if (at % align) return refuse(err, MUON_EINVAL, std::string(name) + ": pointer not aligned to " + std::to_string(align) + " bytes");
-  if (uintptr_t(bytes) > UINTPTR_MAX - at) return refuse(err, MUON_EINVAL, std::string(name) + ": buffer passes the end of memory");
+  // Within the 2^62 bytes that the kernels' 64-bit offsets reach.
+  if (uintptr_t(run) > UINTPTR_MAX - at ||
+      uintptr_t(rows - 1) > std::min<uintptr_t>(UINTPTR_MAX - at - uintptr_t(run), uintptr_t(1) << 62) / uintptr_t(step))
+    return refuse(err, MUON_EINVAL, std::string(name) + ": buffer passes the end of memory");
   return MUON_OK;
 }
 
@@ -70,11 +74,10 @@ int check_view(const char* name, const muon_view* v, Span* span, std::string* er
   if (rc != MUON_OK) return rc;
   *span = {name, reinterpret_cast<uintptr_t>(v->data), v->rows, v->cols * es, v->ld * es};
   if (span->empty()) return MUON_OK;
-  // Rows of up to 2^32 elements: any byte offset fits 64 bits.
   if (v->rows > 1 && (v->ld < v->cols || v->ld > (int64_t(1) << 32)))
     return refuse(err, MUON_EINVAL, std::string(name) + ": ld must be in [cols, 2^32]");
   if (v->rows == 1) span->step = span->run;
-  return check_pointer(name, v->data, uintptr_t(es), (v->rows - 1) * span->step + span->run, err);
+  return check_pointer(name, v->data, uintptr_t(es), v->rows, span->run, span->step, err);
 }
 
 int64_t groups_of(const muon_codes& c) { return c.block ? ceil_div(c.cols, kCodeBlock) : 1; }
@@ -90,8 +93,8 @@ int check_codes(const char* name, const muon_codes* c, int32_t block, Span* q, S
   const int64_t pitch = MUON_CODES_PITCH(c->cols), groups = groups_of(*c);
   *q = {name, reinterpret_cast<uintptr_t>(c->q), c->rows, pitch, pitch};
   *scale = {name, reinterpret_cast<uintptr_t>(c->scale), c->rows, groups * 4, groups * 4};
-  if (!q->empty() && (rc = check_pointer(name, c->q, 16, c->rows * pitch, err)) != MUON_OK) return rc;
-  if (!scale->empty() && (rc = check_pointer(name, c->scale, 4, c->rows * groups * 4, err)) != MUON_OK) return rc;
+  if (!q->empty() && (rc = check_pointer(name, c->q, 16, c->rows, pitch, pitch, err)) != MUON_OK) return rc;
+  if (!scale->empty() && (rc = check_pointer(name, c->scale, 4, c->rows, groups * 4, groups * 4, err)) != MUON_OK) return rc;
   return MUON_OK;
 }
 
@@ -139,9 +142,10 @@ int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
   return splits;
 }
 
-// Which tile: the fewest rounds over the compute units, weighed by what a round takes.  A tile's
-// share of its operands' reads falls with its edges, so a smaller one takes more than its share of
-// a 256 x 256 tile's time: measured per round of FILL.
+// Which tile: the fewest rounds over the compute units, weighed by what a round takes as a part of a
+// round of 256 x 256 tiles (a smaller tile reads more of its operands for each result).  4096
+// columns summed over: 4096 x 4096 results take 64 us in tiles of 256 x 256 and 76 in 256 x 128,
+// 2048 x 4096 take 42 and 39 (46 in 128 x 128), 512 x 4096 39, 27 and 19.
 int int8_tile(int64_t rows, int64_t cols) {
   const int64_t full = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 256), kMaxUnits);
   const int64_t half = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 128), kMaxUnits);

@@ -78,6 +78,8 @@ OUT = BASE + 4 * FAR
     (lambda: quantize(view(-1, 8), codes(4, 8)), nm.MUON_EINVAL),
     (lambda: quantize(view(4, (1 << 30) + 1), codes(4, (1 << 30) + 1)), nm.MUON_EINVAL),
     (lambda: quantize(view(4, 8, at=2 ** 64 - 16), codes(4, 8)), nm.MUON_EINVAL),
+    (lambda: quantize(view(1 << 30, 8, ld=1 << 32, dtype=nm.MUON_F32), codes(1 << 30, 8)), nm.MUON_EINVAL),  # 2^64 bytes
+    (lambda: quantize(view(1 << 30, 8, ld=(1 << 32) + 1), codes(1 << 30, 8)), nm.MUON_EINVAL),
     (lambda: quantize(view(4, 8), codes(8, 4)), nm.MUON_EINVAL),
     (lambda: quantize(view(4, 8), codes(4, 8), 1), nm.MUON_EINVAL),
     (lambda: quantize(view(4, 8), codes(8, 4), 2), nm.MUON_EINVAL),
