@@ -179,7 +179,7 @@ struct RowCoder {
       near = fmaxf(near, fabsf(fmaf(x(i), inverse, kToInt - r)));
       n[i] = __float_as_uint(r);
     }
-    if (near > 0.5f - 0x1p-14f) {
+    if (__builtin_expect(near > 0.5f - 0x1p-14f, 0)) {  // out of the way of the instructions that run
 #pragma unroll
       for (int i = 0; i < N; ++i) n[i] = exact(x(i));
     }
