@@ -255,9 +255,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
         y.load(x, c * 8, a.k);
         tops_of.take(y);
       }
-      uint32_t top = tops_of.all();
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
+      uint32_t top = max64(tops_of.all());
       if (team > 1) {
         if (lane == 0) tops[turn & 1][wave] = top;
         __syncthreads();

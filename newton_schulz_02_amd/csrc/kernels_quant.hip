@@ -13,38 +13,30 @@ using namespace muon;
 
 namespace {
 
-// Maximum over the LANES (a power of two up to 64) neighbouring lanes of each group.
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < LANES; d *= 2) v = max(v, uint32_t(__shfl_xor(int(v), d)));
-  return v;
-}
-
 // Codes of rows.  L lanes take a row together: a wave (four rows to a workgroup), or a workgroup of
 // 256 or 1024 lanes.  The first KEEP chunks of 8 values of each lane stay in registers between the
 // maximum and the codes; longer rows are read again (they come from L2).
 template <typename T, int L, int KEEP>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
-  constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L, kKeep = KEEP;
+  constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L;
   __shared__ uint32_t tops[2][L > 64 ? L / 64 : 1];
   const int lane = threadIdx.x % L;
   const int chunks = a.pitch / 8;
   int turn = 0;
   for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / L; row < a.rows; row += int64_t(gridDim.x) * kRows) {
     const T* x = static_cast<const T*>(a.x) + row * a.ld;
-    Eight<T> v[kKeep];
+    Eight<T> v[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) v[i].load(x, (lane + i * L) * 8, a.cols);
     typename Eight<T>::Tops tops_of;
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) v[i].load(x, (lane + i * L) * 8, a.cols);
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) tops_of.take(v[i]);
-    for (int c = lane + kKeep * L; c < chunks; c += L) {
+    for (int i = 0; i < KEEP; ++i) tops_of.take(v[i]);
+    for (int c = lane + KEEP * L; c < chunks; c += L) {
       Eight<T> w;
       w.load(x, c * 8, a.cols);
       tops_of.take(w);
     }
-    uint32_t top = lanes_max<64>(tops_of.all());
+    uint32_t top = max64(tops_of.all());
     if constexpr (L > 64) {
       // The two halves of `tops` take turns, so one barrier a row is enough.
       if ((threadIdx.x & 63) == 0) tops[turn & 1][threadIdx.x / 64] = top;
@@ -57,9 +49,9 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
     if (lane == 0) a.scale[row] = code.scale();
     int8_t* q = a.q + row * a.pitch;
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i)
+    for (int i = 0; i < KEEP; ++i)
       if (lane + i * L < chunks) store_codes(q + (lane + i * L) * 8, code.eight(v[i]));
-    for (int c = lane + kKeep * L; c < chunks; c += L) {
+    for (int c = lane + KEEP * L; c < chunks; c += L) {
       Eight<T> w;
       w.load(x, c * 8, a.cols);
       store_codes(q + c * 8, code.eight(w));
@@ -91,7 +83,7 @@ __global__ __launch_bounds__(256) void k_quant_blocks(QuantArgs a, int64_t total
     for (int u = 0; u < kUnits; ++u) {
       typename Eight<T>::Tops tops;
       tops.take(v[u]);
-      const uint32_t top = lanes_max<16>(tops.all());
+      const uint32_t top = max16(tops.all());
       if (row[u] >= a.rows) continue;
       const BlockCoder code(top);
       store_codes(a.q + row[u] * a.pitch + c[u] * 8, code.eight(v[u]));
@@ -173,7 +165,7 @@ __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
     const int c = lane * 8 + e;
     const RowCoder code(max(tops[0][c], tops[1][c]), inverses[c]);
     uint32_t w[2];
-    code.codes<8>(w, [&](int u) { return v[u].get(e); });
+    code.template codes<8, Eight<T>::kShort>(w, [&](int u) { return v[u].get(e); });
     tile[c * 33 + sub] = w[0];
     tile[c * 33 + 16 + sub] = w[1];
   }
@@ -245,10 +237,11 @@ int grid_of(int64_t n) { return int(std::min<int64_t>(n, 1 << 20)); }
 
 template <typename T>
 int quant_rows(const QuantArgs& a, hipStream_t s) {
-  // A wave keeps 1024 values in registers, 256 lanes 4096 or 16384.  (A wave for each row of 4096, 8
-  // chunks a lane, took 24.9 us for 8192 bf16 rows; 256 lanes take 20.6.)
+  // A wave keeps 1024 or 2048 values in registers, 256 lanes 4096 or 16384.  (16384 bf16 rows of 2048
+  // take 17.7 us with a wave each and 21.6 with 256 lanes, of 4096 47 and 39.7.)
   const dim3 waves(grid_of((a.rows + 3) / 4)), groups(grid_of(a.rows));
   if (a.pitch <= 1024) hipLaunchKernelGGL((k_quant_rows<T, 64, 2>), waves, dim3(256), 0, s, a);
+  else if (a.pitch <= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64, 4>), waves, dim3(256), 0, s, a);
   else if (a.pitch <= 4096) hipLaunchKernelGGL((k_quant_rows<T, 256, 2>), groups, dim3(256), 0, s, a);
   else if (a.pitch <= 16384) hipLaunchKernelGGL((k_quant_rows<T, 256, 8>), groups, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_quant_rows<T, 1024, 4>), groups, dim3(1024), 0, s, a);

@@ -119,6 +119,20 @@ def test_ties(dtype):
     assert torch.equal(y, (c.q[:, :x.shape[1]].int() * 127).float() * c.scale[:, None])
 
 
+@pytest.mark.parametrize("exponent", [-99, -20, 0, 60, 127])
+def test_every_bf16_quotient(exponent):
+    """Each of the 128 mantissas as a row's largest value, with all values down to 2^-11 of it."""
+    tops = (torch.arange(128, 256, dtype=torch.float64) * 2.0 ** (exponent - 7))[:, None]
+    values = (torch.arange(128, 256, dtype=torch.float64) * 2.0 ** -7)[None, :] * \
+        (2.0 ** torch.arange(exponent - 11, exponent + 1, dtype=torch.float64))[:, None]
+    row = values.reshape(1, -1)
+    x = torch.cat([tops, torch.where(row <= tops, row, -0.0 * row), -torch.where(row <= tops, row, 0.0 * row)], dim=1)
+    x = x.to(BF16).to(DEV)
+    check_codes(nm.quantize(x), x, False)
+    check_codes(nm.quantize(x.t().contiguous(), transpose=True), x, False)
+    check_codes(nm.quantize(x.float()), x, False)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_extreme_values(dtype):
     big, tiny = torch.finfo(dtype).max, 2.0 ** -133 if dtype == BF16 else 2.0 ** -149
