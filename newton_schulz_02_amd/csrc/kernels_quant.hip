@@ -237,12 +237,16 @@ int grid_of(int64_t n) { return int(std::min<int64_t>(n, 1 << 20)); }
 
 template <typename T>
 int quant_rows(const QuantArgs& a, hipStream_t s) {
-  // A wave keeps 1024 or 2048 values in registers, 256 lanes 4096 or 16384.  (16384 bf16 rows of 2048
-  // take 17.7 us with a wave each and 21.6 with 256 lanes, of 4096 47 and 39.7.)
+  // A wave keeps 1024 or 2048 values in registers, 256 lanes 4096 to 16384, no more than the row needs:
+  // the registers decide how many rows are in flight.  (16384 bf16 rows of 2048 take 17.7 us with a
+  // wave each and 21.6 with 256 lanes, of 4096 47 and 39.7; of 11008 100 with room for 12288 and
+  // 128 with room for 16384.)
   const dim3 waves(grid_of((a.rows + 3) / 4)), groups(grid_of(a.rows));
   if (a.pitch <= 1024) hipLaunchKernelGGL((k_quant_rows<T, 64, 2>), waves, dim3(256), 0, s, a);
   else if (a.pitch <= 2048) hipLaunchKernelGGL((k_quant_rows<T, 64, 4>), waves, dim3(256), 0, s, a);
   else if (a.pitch <= 4096) hipLaunchKernelGGL((k_quant_rows<T, 256, 2>), groups, dim3(256), 0, s, a);
+  else if (a.pitch <= 8192) hipLaunchKernelGGL((k_quant_rows<T, 256, 4>), groups, dim3(256), 0, s, a);
+  else if (a.pitch <= 12288) hipLaunchKernelGGL((k_quant_rows<T, 256, 6>), groups, dim3(256), 0, s, a);
   else if (a.pitch <= 16384) hipLaunchKernelGGL((k_quant_rows<T, 256, 8>), groups, dim3(256), 0, s, a);
   else hipLaunchKernelGGL((k_quant_rows<T, 1024, 4>), groups, dim3(1024), 0, s, a);
   return hipGetLastError();

@@ -70,7 +70,7 @@ def check_codes(c, x, block):
 
 # Lengths around the vector, block, wave and workgroup sizes of the kernels, and past each variant's.
 SHAPES = [(1, 1), (3, 7), (1, 8), (5, 127), (4, 128), (2, 129), (130, 64), (9, 511), (3, 2048), (2, 2049), (7, 4096),
-          (2, 8192), (1, 8200), (3, 33000), (1, 131071), (257, 385), (1000, 96)]
+          (2, 8192), (1, 8200), (2, 12289), (3, 33000), (1, 131071), (257, 385), (1000, 96)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
