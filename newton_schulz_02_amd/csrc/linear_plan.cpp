@@ -134,7 +134,7 @@ int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
   const double steps = double(ceil_div(a.tokens, 64)), bytes = 8.0 * a.n * a.k;
   double best = step * steps * std::max(1.0, double(tiles) / 384);
   int32_t splits = 1;
-  for (int32_t s = 2; s <= 64 && s <= steps / 2 && tiles * s <= 3 * kMaxUnits; ++s) {
+  for (int32_t s = 2; s <= 64 && s <= steps / (bf16 ? 2 : 1) && tiles * s <= 3 * kMaxUnits; ++s) {
     const double t = step * double(ceil_div(int64_t(steps), s)) * std::max(1.0, double(tiles * s) / 384) + 3.0 + 0.1 * s +
                      s * bytes / 5e6;
     if (t < best) best = t, splits = s;
