@@ -143,17 +143,24 @@ __device__ __forceinline__ void int8_tile(const IntArgs& a) {
     wait_vm<3 * kLoads>();
     stage_barrier();
     read(s0, 0, 0);
-    for (int ks = 0;; ks += 5) {
-      step(ks, s0, s1, s4);
-      if (ks + 1 >= steps) break;
-      step(ks + 1, s1, s2, s0);
-      if (ks + 2 >= steps) break;
-      step(ks + 2, s2, s3, s1);
-      if (ks + 3 >= steps) break;
-      step(ks + 3, s3, s4, s2);
-      if (ks + 4 >= steps) break;
-      step(ks + 4, s4, s0, s3);
-      if (ks + 5 >= steps) break;
+    auto step_at = [&](int ks, auto at) {
+      constexpr int i = decltype(at)::value;
+      char* const st[kStages] = {s0, s1, s2, s3, s4};
+      step(ks, st[i], st[(i + 1) % kStages], st[(i + 4) % kStages]);
+    };
+    // Five steps until the stages come round, and the rest behind the loop: with exits inside it the
+    // compiler joined their states with the next round's, and waited for all loads there.
+    int ks = 0;
+    for (; ks + kStages <= steps; ks += kStages) static_for<kStages>([&](auto at) { step_at(ks + decltype(at)::value, at); });
+    if (ks < steps) {
+      step_at(ks, std::integral_constant<int, 0>{});
+      if (ks + 1 < steps) {
+        step_at(ks + 1, std::integral_constant<int, 1>{});
+        if (ks + 2 < steps) {
+          step_at(ks + 2, std::integral_constant<int, 2>{});
+          if (ks + 3 < steps) step_at(ks + 3, std::integral_constant<int, 3>{});
+        }
+      }
     }
     wait_vm<0>();  // what the last steps loaded
   }

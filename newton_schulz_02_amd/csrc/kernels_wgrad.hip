@@ -280,19 +280,30 @@ __device__ __forceinline__ void wgrad_tile(const WgradArgs& a) {
     for (int p = 0; p < 2 * kUnits; ++p) put_x(0, x0, p >> 1, p & 1, b0);
 #pragma unroll
     for (int kk = 0; kk < kGroups; ++kk) load_share(1, kk, a1, x1, a0);
-    for (int ks = 0;; ks += 6) {
-      step(ks, a0, b0, a1, a2, b1, x0, x1);
-      if (ks + 1 >= steps) break;
-      step(ks + 1, a1, b1, a2, a0, b0, x1, x0);
-      if (ks + 2 >= steps) break;
-      step(ks + 2, a2, b0, a0, a1, b1, x0, x1);
-      if (ks + 3 >= steps) break;
-      step(ks + 3, a0, b1, a1, a2, b0, x1, x0);
-      if (ks + 4 >= steps) break;
-      step(ks + 4, a1, b0, a2, a0, b1, x0, x1);
-      if (ks + 5 >= steps) break;
-      step(ks + 5, a2, b1, a0, a1, b0, x1, x0);
-      if (ks + 6 >= steps) break;
+    auto step_at = [&](int ks, auto at) {
+      constexpr int i = decltype(at)::value;
+      char* const st[3] = {a0, a1, a2};
+      char* const sx[2] = {b0, b1};
+      const std::integral_constant<int, i % 2> set{};
+      const std::integral_constant<int, 1 - i % 2> other{};
+      step(ks, st[i % 3], sx[i % 2], st[(i + 1) % 3], st[(i + 2) % 3], sx[1 - i % 2], set, other);
+    };
+    // Six steps until stages and registers come round, and the rest behind the loop: with exits inside
+    // it the compiler joined their states with the next round's, and waited for all loads there.
+    int ks = 0;
+    for (; ks + 6 <= steps; ks += 6) static_for<6>([&](auto at) { step_at(ks + decltype(at)::value, at); });
+    if (ks < steps) {
+      step_at(ks, std::integral_constant<int, 0>{});
+      if (ks + 1 < steps) {
+        step_at(ks + 1, std::integral_constant<int, 1>{});
+        if (ks + 2 < steps) {
+          step_at(ks + 2, std::integral_constant<int, 2>{});
+          if (ks + 3 < steps) {
+            step_at(ks + 3, std::integral_constant<int, 3>{});
+            if (ks + 4 < steps) step_at(ks + 4, std::integral_constant<int, 4>{});
+          }
+        }
+      }
     }
     wait_vm<0>();  // what the last step loaded
   }
