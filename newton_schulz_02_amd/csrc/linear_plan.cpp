@@ -127,16 +127,20 @@ bool quant_too_large(const QuantPlan& p) {
 }
 
 // Few tiles: the tokens are cut into pieces, whose partial results a second launch joins.  In
-// microseconds: a step of 64 tokens takes 0.66 (fp32 dy: 4.5) where the workgroups share no compute
-// unit, a join 3, a tenth for each piece and its bytes at 5 TB/s.
+// microseconds: a step of 64 tokens takes 0.63 where each workgroup has a compute unit and 0.8 where
+// some share one (fp32 dy: 4.5, and two share one with little loss); a join takes 1.7, a tenth for each
+// piece and its bytes at 5 TB/s.  (777 tokens, 517 x 1031 results: 17.0 whole, 15.5 in the 3 pieces
+// that this chooses; 8192, 768 x 768: 85.6 whole, 24.3 in 6, 27.6 in 8.)
 int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
-  const double step = bf16 ? 0.66 : 4.5;
   const double steps = double(ceil_div(a.tokens, 64)), bytes = 8.0 * a.n * a.k;
-  double best = step * steps * std::max(1.0, double(tiles) / 384);
+  auto step = [&](int64_t groups) {
+    if (!bf16) return 4.5 * std::max(1.0, double(groups) / 384);
+    return groups <= kMaxUnits ? 0.63 : 0.8 * std::max(1.0, double(groups) / (2 * kMaxUnits));
+  };
+  double best = step(tiles) * steps;
   int32_t splits = 1;
   for (int32_t s = 2; s <= 64 && s <= steps / (bf16 ? 2 : 1) && tiles * s <= 3 * kMaxUnits; ++s) {
-    const double t = step * double(ceil_div(int64_t(steps), s)) * std::max(1.0, double(tiles * s) / 384) + 3.0 + 0.1 * s +
-                     s * bytes / 5e6;
+    const double t = step(tiles * s) * double(ceil_div(int64_t(steps), s)) + 1.7 + 0.1 * s + s * bytes / 5e6;
     if (t < best) best = t, splits = s;
   }
   return splits;
@@ -290,7 +294,6 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
     const int64_t tiles128 = ceil_div(a.n, 128) * ceil_div(a.k, 128), tiles256 = ceil_div(a.n, 256) * ceil_div(a.k, 256);
     if (tiles128 > (1 << 23)) return refuse(err, MUON_EINVAL, "the result is too large");
     if (p->bf16 && tiles256 >= 192) p->tile = kTile256;
-    const int64_t tiles = p->tile == kTile256 ? tiles256 : tiles128;
     // bf16 rows go to LDS 16 bytes at a time, by 32-bit offsets from the first of 64 tokens.  Others
     // come through registers, in small tiles, or are copied first (517 x 1031 from 777 tokens: 15 us
     // through registers, 20 with the copy).
@@ -307,7 +310,9 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
       a.n_read = int32_t(p->pack_ld);
       p->buf.ws_bytes = size_t(round_up(a.tokens * p->pack_ld * 2, 256));
     }
-    a.splits = wgrad_splits(tiles, a, p->bf16);
+    // Tiles of 256 x 256 keep three quarters of the compute units busy or more, and these draw what power
+    // there is: they are not cut (4096 x 3000 results, 16384 tokens: 376 us whole, 430 in 2 pieces).
+    if (p->tile != kTile256) a.splits = wgrad_splits(tiles128, a, p->bf16);
     if (a.splits > 1) {
       a.piece = int32_t(round_up(ceil_div(a.tokens, a.splits), 64));
       a.splits = int32_t(ceil_div(a.tokens, a.piece));
