@@ -277,6 +277,29 @@ def test_weight_grads_of_whole_numbers(tokens, outputs, inputs, dtype):
     assert torch.equal(nm.weight_grad(dy, kept, BF16), want.to(BF16))
 
 
+@pytest.mark.parametrize("outputs,inputs,shift", [(1024, 2048, 0), (1021, 2048, 1), (3592, 3600, 0)])
+def test_weight_grads_of_any_number_of_steps(outputs, inputs, shift):
+    """1 to 13 steps of 64 tokens: rounds of six and every rest, in each kind of tile.  Exact."""
+    for steps in range(1, 14):
+        log(f"weight grad {steps} steps of {outputs}x{inputs}")
+        tokens = 64 * steps - 3 * (steps % 2)
+        dy, x = whole(tokens, outputs, 7, BF16, steps, 0, shift), whole(tokens, inputs, 7, BF16, 20 + steps)
+        want = dy.float().t().contiguous() @ x.float()  # below 49 * 832: exact
+        assert torch.equal(nm.weight_grad(dy, nm.quantize(x, block=True)), want)
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 200), (2048, 4096), (4096, 4096)])
+def test_products_of_any_number_of_steps(rows, cols):
+    """2 to 14 steps of 64 columns: rounds of five and every rest, in each tile.  With 127 in each row the
+    codes are the values, and sums stay below 127^2 + 49 * 896 < 2^24: exact."""
+    for k in range(128, 128 * 8, 128):
+        log(f"int8 product {rows}x{cols}x{k}")
+        a, b = whole(rows, k, 7, BF16, k), whole(cols, k, 7, BF16, k + 1)
+        a[:, 0] = b[:, 0] = 127
+        got = nm.int8_matmul(nm.quantize(a), nm.quantize(b), F32)
+        assert torch.equal(got, a.float() @ b.float().t().contiguous())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,outputs,inputs", [(1, 5, 300), (100, 64, 257), (1500, 136, 384), (640, 3640, 3520)])
 def test_weight_grads(tokens, outputs, inputs, dtype):
