@@ -1094,6 +1094,7 @@ def adamw_list_step(params, grads, ms, vs, *, step=1, clip=None, stream=None, **
 
 
 # --- 8-bit operators of linear layers (include/muon_linear.h) ----------------------------
+# The steps of a forward and a backward pass, as calls: none records an autograd graph.
 
 CODE_BLOCK = 128  #: columns of a block scale; rows of codes are padded to a multiple of it
 

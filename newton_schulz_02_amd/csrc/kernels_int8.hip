@@ -6,6 +6,10 @@
 // one of five stages in LDS, so loads have three steps to arrive, and step ks + 1 is complete
 // when step ks begins: the last group of step ks reads the first fragments of the next one, and
 // matrix instructions (v_mfma_i32_32x32x32_i8; the sums are exact) go on over the barrier.
+//
+// 16384 x 11008 x 4096 take 630 to 660 us (2.3 POP/s), 8192^3 445 (2.5): bound by power, at 1.6 GHz with
+// the matrix units busy 64 % of the time.  2048 x 4096 x 4096 take 39 us in 256 x 128 tiles, bound by LDS
+// accesses, of which a tile of half the results needs two thirds.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -203,8 +207,10 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_int8(IntArgs a) {
 // 8 waves takes 16 C columns and up to 16 G rows; wave w takes the k-steps w, w + 8, ... of 128
 // bytes, a lane 16 bytes of each half of one row of each operand, kAhead steps before they are
 // multiplied.
-// Partial sums are integers and meet in LDS.  With FUSED the rows come as values and every
-// workgroup makes their codes itself, in LDS, while its first loads of B are on their way.
+// Partial sums are integers and meet in LDS.  One row of 4096 for 11008 columns takes 12 us (3.8 TB/s):
+// the weights, and about 3 us until the first arrive and the sums have met.
+// With FUSED the rows come as values and every workgroup makes their codes itself, in LDS, while its
+// first loads of B are on their way.
 constexpr int kFewWaves = 8;
 template <bool FUSED, typename T, int G, int C>
 __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {

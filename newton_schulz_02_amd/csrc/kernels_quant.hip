@@ -15,7 +15,8 @@ namespace {
 
 // Codes of rows.  L lanes take a row together: a wave (four rows to a workgroup), or a workgroup of
 // 256 or 1024 lanes.  The first KEEP chunks of 8 values of each lane stay in registers between the
-// maximum and the codes; longer rows are read again (they come from L2).
+// maximum and the codes; longer rows are read again (they come from L2).  16384 x 4096 bf16 take 36 us
+// (5.6 TB/s), 16384 x 11008 100 us (5.4).
 template <typename T, int L, int KEEP>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
   constexpr int kThreads = L < 256 ? 256 : L, kRows = kThreads / L;
@@ -60,7 +61,8 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void k_quant_rows(QuantArgs a) {
 }
 
 // Codes of blocks: 16 lanes take a block of 128 values, so a wave reads 1 KB (bf16) at once.  A
-// workgroup takes kUnits x 256 consecutive chunks of 8 values, all in flight together.
+// workgroup takes kUnits x 256 consecutive chunks of 8 values, all in flight together.  16384 x 11008
+// bf16 take 92 us (5.9 TB/s).
 constexpr int kUnits = 4;
 template <typename T>
 __global__ __launch_bounds__(256) void k_quant_blocks(QuantArgs a, int64_t total) {
@@ -95,7 +97,8 @@ __global__ __launch_bounds__(256) void k_quant_blocks(QuantArgs a, int64_t total
 }
 
 // Codes of columns, first launch: parts[s][c] <- the maximum of column c over row strip s of x.
-// A workgroup takes 256 columns (32 lanes of 8) and 8 rows at a time.
+// A workgroup takes 256 columns (32 lanes of 8) and 8 rows at a time.  11008 x 4096 bf16 take 19 us
+// (4.8 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void k_quant_cols_max(QuantArgs a) {
   __shared__ uint32_t tops[8][256 + 8];
@@ -127,7 +130,8 @@ __global__ __launch_bounds__(256) void k_quant_cols_max(QuantArgs a) {
 
 // Second launch: 128 columns of x by 128 rows to 128 rows of codes by 128, through LDS.  A lane
 // has 8 columns and, at a time, 4 consecutive rows: four codes of one column go to LDS as one
-// word.  Rows of 33 words: the words of neighbouring lanes lie 8 banks apart.
+// word.  Rows of 33 words: the words of neighbouring lanes lie 8 banks apart.  11008 x 4096 bf16 take
+// 25 us (5.4 TB/s), x coming in part from the cache that the first launch filled.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
   __shared__ uint32_t tile[128 * 33];
@@ -180,7 +184,7 @@ __global__ __launch_bounds__(256) void k_quant_cols(QuantArgs a) {
 }
 
 // Values of codes: a lane takes 16 bytes of the result, 8 or 4 codes of one row, so that a wave
-// writes whole lines.
+// writes whole lines.  16384 x 11008 to bf16 take 95 us (5.7 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequant(DequantArgs a, int64_t total) {
   constexpr int E = Run<T>::E;
@@ -239,7 +243,7 @@ template <typename T>
 int quant_rows(const QuantArgs& a, hipStream_t s) {
   // A wave keeps 1024 or 2048 values in registers, 256 lanes 4096 to 16384, no more than the row needs:
   // the registers decide how many rows are in flight.  (16384 bf16 rows of 2048 take 17.7 us with a
-  // wave each and 21.6 with 256 lanes, of 4096 47 and 39.7; of 11008 100 with room for 12288 and
+  // wave each and 21.6 with 256 lanes, of 4096 then 47 and 39.7; of 11008 100 with room for 12288 and
   // 128 with room for 16384.)
   const dim3 waves(grid_of((a.rows + 3) / 4)), groups(grid_of(a.rows));
   if (a.pitch <= 1024) hipLaunchKernelGGL((k_quant_rows<T, 64, 2>), waves, dim3(256), 0, s, a);
