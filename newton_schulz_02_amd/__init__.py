@@ -1094,7 +1094,8 @@ def adamw_list_step(params, grads, ms, vs, *, step=1, clip=None, stream=None, **
 
 
 # --- 8-bit operators of linear layers (include/muon_linear.h) ----------------------------
-# The steps of a forward and a backward pass, as calls: none records an autograd graph.
+# The steps of a forward and a backward pass, as calls.  None records an autograd graph, so an
+# operand that needs a gradient is refused where torch would record one.
 
 CODE_BLOCK = 128  #: columns of a block scale; rows of codes are padded to a multiple of it
 
@@ -1117,7 +1118,7 @@ class Codes:
             raise ValueError(f"q must be contiguous int8 of rows x {-(-cols // CODE_BLOCK) * CODE_BLOCK}")
         if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() != rows * groups:
             raise ValueError(f"scale must be contiguous float32 of {rows} x {groups} values")
-        self.device = _linear_device(q, scale)
+        self.device = _linear_device(torch, q, scale)
         self.block, self.shape, self._memory, self._q, self._scale = bool(block), (rows, cols), (q, scale), q, scale
         self._arg = muon_codes(q.data_ptr(), scale.data_ptr(), rows, cols, CODE_BLOCK if block else 0, 0)
 
@@ -1165,6 +1166,11 @@ class Codes:
             self._views()
         return self._scale
 
+    @property
+    def requires_grad(self) -> bool:
+        """Whether the scales do (codes are integers)."""
+        return self._scale is not None and self._scale.requires_grad
+
     def record_stream(self, stream) -> None:
         """Keep the memory until `stream` has passed what it has been given so far."""
         for t in self._memory:
@@ -1175,15 +1181,25 @@ class Codes:
         return dequantize(self, dtype, out=out, stream=stream)
 
 
-def _linear_device(first, *others):
-    """The one GPU that tensors (or Codes) are on."""
-    device = first.device
+def _linear_device(torch, *operands):
+    """The one GPU that tensors (or Codes) are on; none of them may need a gradient."""
+    device, tangents = operands[0].device, torch.autograd.forward_ad._current_level >= 0
+    for t in operands:
+        if t is None:
+            continue
+        if t.requires_grad and torch.is_grad_enabled() or tangents and _has_tangent(torch, t):
+            raise ValueError("an operand needs a gradient or has a tangent, and the 8-bit operators record neither: call "
+                             "them from a torch.autograd.Function, or under torch.no_grad() without a tangent")
+        if t.device != device:
+            raise ValueError(f"operands must be on one GPU, not on {device} and {t.device}")
     if device.type != "cuda":
         raise ValueError(f"operands must be on a GPU, not on {device}")
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"operands must be on one GPU, not on {device} and {t.device}")
     return device
+
+
+def _has_tangent(torch, t) -> bool:
+    t = t._scale if isinstance(t, Codes) else t
+    return t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None
 
 
 def _view_arg(name, t):
@@ -1304,10 +1320,14 @@ def quantize(x, *, block=False, transpose=False, out=None, stream=None) -> Codes
     127 x / max|row|.  With block=True (a checkpoint, for weight_grad) by 128 columns of a row,
     with the smallest power of two that fits them as the scale.  transpose=True gives the codes
     of x's columns, as rows (codes by row only): a weight's for the input gradient.  `out`: Codes
-    to write to.  A row or block with a NaN or an infinity stands for NaN."""
+    to write to.  A row or block with a NaN or an infinity stands for NaN.
+
+    This and the other 8-bit operators record no autograd graph: operands that need a gradient
+    are refused unless gradients are off (torch.no_grad(), a torch.autograd.Function), and operands
+    with a forward-mode tangent always."""
     import torch
 
-    device = _linear_device(x, out)
+    device = _linear_device(torch, x, out)
     xv = _view_arg("x", x)
     shape = (xv.cols, xv.rows) if transpose else (xv.rows, xv.cols)
     if block and transpose:
@@ -1329,7 +1349,7 @@ def dequantize(codes, dtype=None, *, out=None, stream=None):
     """The values that codes stand for, code * scale, in bfloat16 (default) or float32."""
     import torch
 
-    device = _linear_device(codes, out)
+    device = _linear_device(torch, codes, out)
     out = _linear_out(out, codes.shape, dtype, torch.bfloat16, device, stream)
     _linear_call(lib().muon_dequantize, (codes._arg, _view_arg("out", out)), None, device, stream, (codes, out))
     return out
@@ -1340,7 +1360,7 @@ def int8_matmul(a, b, dtype=None, *, out=None, stream=None):
     32-bit integers, times the scales of token and channel, in bfloat16 (default) or float32."""
     import torch
 
-    device = _linear_device(a, b, out)
+    device = _linear_device(torch, a, b, out)
     (rows, k), cols = a.shape, b.shape[0]
     need = _matmul_need(rows, cols, k)
     out = _linear_out(out, (rows, cols), dtype, torch.bfloat16, device, stream)
@@ -1351,7 +1371,9 @@ def int8_matmul(a, b, dtype=None, *, out=None, stream=None):
 def int8_linear(x, w, dtype=None, *, out=None, stream=None):
     """int8_matmul(quantize(x), w), bit for bit, in x's dtype by default; for a few rows of x in one
     launch."""
-    device = _linear_device(x, w, out)
+    import torch
+
+    device = _linear_device(torch, x, w, out)
     xv, cols = _view_arg("x", x), w.shape[0]
     need = _linear_need(xv.rows, cols, xv.cols, xv.dtype)
     out = _linear_out(out, (xv.rows, cols), dtype, x.dtype, device, stream)
@@ -1365,7 +1387,7 @@ def weight_grad(dy, x, dtype=None, *, out=None, accumulate=False, stream=None):
     accumulate=True it is added to `out`, the gradient so far."""
     import torch
 
-    device = _linear_device(dy, x, out)
+    device = _linear_device(torch, dy, x, out)
     if accumulate and out is None:
         raise ValueError("accumulate needs out, the gradient to add to")
     dv, inputs = _view_arg("dy", dy), x.shape[1]

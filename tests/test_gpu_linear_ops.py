@@ -559,3 +559,44 @@ def test_results_behind_2_31_elements():
     del dw
     t = nm.quantize(whole(40000, 54001, 7, BF16, 3), transpose=True)
     assert torch.equal(t.q[-70:, :40000].t(), nm.quantize(whole(40000, 54001, 7, BF16, 3)[:, -70:], transpose=True).q[:, :40000].t())
+
+
+class Layer(torch.autograd.Function):
+    """A linear layer as a user of autograd has it: y = x W^T, in 8 bits both ways."""
+
+    @staticmethod
+    def forward(ctx, x, w):
+        ctx.kept = nm.quantize(x, block=True)
+        ctx.save_for_backward(w)
+        return nm.int8_linear(x, nm.quantize(w))
+
+    @staticmethod
+    def backward(ctx, dy):
+        (w,) = ctx.saved_tensors
+        return nm.int8_linear(dy, nm.quantize(w, transpose=True)), nm.weight_grad(dy, ctx.kept, BF16)
+
+
+def test_a_layer_for_autograd():
+    x, w, dy = normal(200, 264, BF16, 1), normal(136, 264, BF16, 2), normal(200, 136, BF16, 3)
+    want = nm.int8_linear(x, nm.quantize(w))
+    dx = nm.int8_linear(dy, nm.quantize(w, transpose=True))
+    dw = nm.weight_grad(dy, nm.quantize(x, block=True), BF16)
+    x, w = x.clone().requires_grad_(), w.clone().requires_grad_()
+    y = Layer.apply(x, w)
+    y.backward(dy)
+    assert torch.equal(y, want) and torch.equal(x.grad, dx) and torch.equal(w.grad, dw)
+
+
+def test_operands_that_need_a_gradient_are_refused():
+    x, w = normal(4, 300, F32, 1), nm.quantize(normal(8, 300, F32, 2))
+    leaf, y = x.clone().requires_grad_(), torch.full((4, 8), 5.0, device=DEV)
+    kept, learned = nm.quantize(x, block=True), nm.quantize(normal(8, 300, F32, 2))
+    learned.scale.requires_grad_()
+    for call in (lambda: nm.int8_linear(leaf, w, out=y), lambda: nm.int8_linear(x, learned, out=y), lambda: learned.dequantize(),
+                 lambda: nm.int8_matmul(nm.quantize(x), learned, out=y), lambda: nm.quantize(leaf * 2),
+                 lambda: nm.weight_grad(leaf[:, :5], kept)):
+        with pytest.raises(ValueError, match="needs a gradient"):
+            call()
+    assert (y == 5.0).all()
+    with torch.no_grad():
+        assert torch.equal(nm.int8_linear(leaf, learned), nm.int8_linear(x, w))

@@ -198,6 +198,64 @@ def test_binding_refusals(call, kind):
         call(torch.zeros(4, 8))
 
 
+def leaf(*shape):
+    return torch.zeros(*shape).requires_grad_()
+
+
+CALLS_WITH_A_GRADIENT = [
+    lambda x: nm.quantize(x),
+    lambda x: nm.quantize(x, block=True),
+    lambda x: nm.quantize(x * 2.0, transpose=True),  # not a leaf
+    lambda x: nm.quantize(torch.zeros(4, 8), out=x),
+    lambda x: nm.dequantize(x.detach(), out=x),
+    lambda x: nm.int8_matmul(x, x.detach()),
+    lambda x: nm.int8_matmul(x.detach(), x),
+    lambda x: nm.int8_linear(x, x.detach()),
+    lambda x: nm.int8_linear(x.detach(), x.detach(), out=x),
+    lambda x: nm.weight_grad(x, x.detach()),
+    lambda x: nm.weight_grad(x.detach(), x.detach(), out=x, accumulate=True),
+    lambda x: nm.Codes(torch.zeros(4, 128, dtype=torch.int8), leaf(4), 8),
+]
+
+
+@pytest.mark.parametrize("call", CALLS_WITH_A_GRADIENT)
+def test_operands_that_need_a_gradient_are_refused(call):
+    """The calls record no graph: a gradient would be lost without a word."""
+    with pytest.raises(ValueError, match="needs a gradient"):
+        call(leaf(4, 8))
+    with torch.no_grad(), pytest.raises(ValueError, match="on a GPU"):  # as of any tensor here
+        call(leaf(4, 8))
+
+
+@pytest.mark.parametrize("call", CALLS_WITH_A_GRADIENT[:-1])
+def test_operands_with_a_tangent_are_refused(call):
+    with torch.autograd.forward_ad.dual_level():
+        x = torch.autograd.forward_ad.make_dual(torch.zeros(4, 8), torch.ones(4, 8))
+        x.detach = lambda: torch.zeros(4, 8)  # keeps a tangent otherwise
+        with torch.no_grad(), pytest.raises(ValueError, match="needs a gradient"):
+            call(x)
+
+
+def test_a_function_may_call_the_operators():
+    """Inside a torch.autograd.Function gradients are off: the call goes on to its other checks."""
+    class Layer(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            with pytest.raises(ValueError, match="on a GPU"):
+                nm.quantize(x, block=True)
+            return x.clone()
+
+        @staticmethod
+        def backward(ctx, dy):
+            with pytest.raises(ValueError, match="on a GPU"):
+                nm.weight_grad(dy, dy)
+            return dy
+
+    x = leaf(4, 8)
+    Layer.apply(x).sum().backward()
+    assert x.grad.eq(1).all()
+
+
 def test_views_of_single_rows_and_columns():
     x = torch.zeros(6, 8)
     for t, want in ((x[:, 2:5], (6, 3, 8)), (x[:1].expand(1, 8), (1, 8, 8)), (x[:, :1], (6, 1, 8)),
