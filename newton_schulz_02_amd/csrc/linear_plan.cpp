@@ -72,11 +72,13 @@ int check_view(const char* name, const muon_view* v, Span* span, std::string* er
   if (v->reserved != 0) return refuse(err, MUON_EINVAL, std::string(name) + ": reserved field must be 0");
   const int rc = check_size(name, v->rows, v->cols, err);
   if (rc != MUON_OK) return rc;
-  *span = {name, reinterpret_cast<uintptr_t>(v->data), v->rows, v->cols * es, v->ld * es};
+  *span = {name, reinterpret_cast<uintptr_t>(v->data), v->rows, v->cols * es, v->cols * es};
   if (span->empty()) return MUON_OK;
-  if (v->rows > 1 && (v->ld < v->cols || v->ld > (int64_t(1) << 32)))
-    return refuse(err, MUON_EINVAL, std::string(name) + ": ld must be in [cols, 2^32]");
-  if (v->rows == 1) span->step = span->run;
+  if (v->rows > 1) {
+    if (v->ld < v->cols || v->ld > (int64_t(1) << 32))
+      return refuse(err, MUON_EINVAL, std::string(name) + ": ld must be in [cols, 2^32]");
+    span->step = v->ld * es;
+  }
   return check_pointer(name, v->data, uintptr_t(es), v->rows, span->run, span->step, err);
 }
 

@@ -6,6 +6,8 @@ made only where no GPU is visible (they then stop at the first HIP call)."""
 from __future__ import annotations
 
 import ctypes
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -314,3 +316,27 @@ def test_oracle_gradient_is_the_difference_quotient():
         e = np.zeros_like(w)
         e[i, j] = 1.0
         assert abs((loss(w + e) - loss(w - e)) / 2 - dw[i, j]) < 1e-10
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_row_distances_of_any_size_are_looked_at_without_overflow(tmp_path):
+    """The host's checks, compiled to stop at a signed overflow: ld is free where there is one row (or
+    none), and refused beyond [cols, 2^32] otherwise."""
+    (tmp_path / "main.cpp").write_text("""
+        #include "linear_plan.h"
+        int main() {
+          std::string err;
+          muon::QuantPlan p;
+          for (int64_t ld : {INT64_MAX, INT64_MIN, int64_t(1) << 62, -(int64_t(1) << 61), int64_t(1) << 33, int64_t(7)})
+            for (int32_t dtype : {MUON_BF16, MUON_F32})
+              for (int64_t rows = 0; rows < 3; ++rows) {
+                const muon_view x = {reinterpret_cast<void*>(uintptr_t(1) << 40), rows, 8, ld, dtype, 0};
+                if (muon::plan_quantize(&x, 0, nullptr, &p, &err) != (rows > 1 ? MUON_EINVAL : MUON_OK)) return 1;
+              }
+          return 0;
+        }""")
+    subprocess.run(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", f"-I{build.CSRC}",
+                    str(tmp_path / "main.cpp"), str(build.CSRC / "linear_plan.cpp"), "-o", str(tmp_path / "main")],
+                   check=True, timeout=120)
+    run = subprocess.run([str(tmp_path / "main")], capture_output=True, text=True, timeout=60)
+    assert run.returncode == 0, run.stderr
