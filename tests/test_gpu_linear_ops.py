@@ -561,6 +561,53 @@ def test_results_behind_2_31_elements():
     assert torch.equal(t.q[-70:, :40000].t(), nm.quantize(whole(40000, 54001, 7, BF16, 3)[:, -70:], transpose=True).q[:, :40000].t())
 
 
+def same_codes(c, part, lo, hi):
+    return torch.equal(c.q[lo:hi], part.q) and torch.equal(c.scale[lo:hi], part.scale)
+
+
+@pytest.mark.parametrize("cols", [1, 2049])
+def test_more_rows_than_workgroups(cols):
+    """A launch of codes by row has at most 2^20 workgroups, of four rows (a wave each) or one; longer
+    operands go round three times here.  A part of one round at a time gives the same."""
+    turn = (4 if cols == 1 else 1) << 20
+    rows = 2 * turn + 19
+    x = torch.empty(rows, cols, device=DEV, dtype=BF16).normal_(generator=gen(1))
+    c = nm.quantize(x)
+    for at in range(0, rows, turn):
+        hi = min(rows, at + turn)
+        log(f"rows {at} to {hi} of {cols}")
+        assert same_codes(c, nm.quantize(x[at:hi]), at, hi)
+    check_codes(nm.quantize(x[-100:]), x[-100:], False)
+
+
+def test_more_blocks_than_workgroups():
+    """The same of codes by block (2^30 runs of 8 values in 2^20 workgroups) and of reading them."""
+    rows, turn = (1 << 26) + 100, 1 << 25
+    x = torch.empty(rows, 128, device=DEV, dtype=BF16).normal_(generator=gen(1))
+    c = nm.quantize(x, block=True)
+    values = c.dequantize(BF16)
+    for at in range(0, rows, turn):
+        hi = min(rows, at + turn)
+        log(f"rows {at} to {hi}")
+        part = nm.quantize(x[at:hi], block=True)
+        assert same_codes(c, part, at, hi)
+        assert torch.equal(values[at:hi], part.dequantize(BF16))
+        del part
+    check_codes(nm.quantize(x[-100:], block=True), x[-100:], True)
+
+
+def test_more_unaligned_rows_than_workgroups():
+    """Rows of dy that are copied to aligned ones first, 2^28 runs of 8 values in a round."""
+    tokens, outputs = (1 << 24) + 50, 121
+    dy = torch.zeros(tokens, outputs, device=DEV, dtype=BF16)
+    x = torch.zeros(tokens, 3, device=DEV, dtype=BF16)
+    ends = torch.cat([torch.arange(60), torch.arange(tokens - 110, tokens)]).to(DEV)
+    dy[ends], x[ends] = whole(170, outputs, 7, BF16, 1), whole(170, 3, 7, BF16, 2)
+    x[60:-110] = 5.0
+    want = dy[ends].double().t().contiguous() @ x[ends].double()
+    assert torch.equal(nm.weight_grad(dy, nm.quantize(x, block=True)).double(), want)
+
+
 class Layer(torch.autograd.Function):
     """A linear layer as a user of autograd has it: y = x W^T, in 8 bits both ways."""
 
