@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
   constexpr int kAhead = C == 1 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char codes[];  // FUSED: rows x pitch
   __shared__ int sums[kFewWaves][16 * C][16 * G + 1];
-  __shared__ uint32_t tops[2][kFewWaves];
+  __shared__ uint32_t tops[kFewWaves];
   __shared__ float scales[16 * G];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col0 = int(blockIdx.x) * 16 * C;
@@ -242,8 +242,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
   };
   if constexpr (FUSED) {
     // The waves in groups of `team`, each with one row at a time, whose first kHold chunks of 8 values a
-    // lane are kept between the maximum and the codes.  Loads arrive in their order, so the first
-    // rows are asked for before B (behind it, the codes were begun when all of B had come).
+    // lane are kept between the maximum and the codes.  Where a team is more than a wave (up to 4 rows)
+    // there is a team for each row, so the loop runs once and `tops` is written once.  Loads arrive in
+    // their order, so the first rows are asked for before B (behind it, the codes were begun when all
+    // of B had come).
     constexpr int kHold = 2;
     const int team = a.rows == 1 ? kFewWaves : a.rows == 2 ? kFewWaves / 2 : a.rows <= 4 ? kFewWaves / 4 : 1;
     const int at_once = kFewWaves / team;
@@ -256,7 +258,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
     };
     load_row(row_of(wave / team));
     load_first();
-    for (int r0 = 0, turn = 0; r0 < a.rows; r0 += at_once, ++turn) {
+    for (int r0 = 0; r0 < a.rows; r0 += at_once) {
       const int row = r0 + wave / team;
       const T* x = row_of(row);
       if (r0 > 0) load_row(x);
@@ -270,9 +272,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_int8_few(IntArgs a) {
       }
       uint32_t top = max64(tops_of.all());
       if (team > 1) {
-        if (lane == 0) tops[turn & 1][wave] = top;
+        if (lane == 0) tops[wave] = top;
         __syncthreads();
-        for (int i = 0; i < team; ++i) top = max(top, tops[turn & 1][wave / team * team + i]);
+        for (int i = 0; i < team; ++i) top = max(top, tops[wave / team * team + i]);
       }
       if (row < a.rows) {
         const RowCoder code(top);
