@@ -399,34 +399,35 @@ __global__ __launch_bounds__(256, 2) void k_wgrad_f32(WgradArgs a) {
   put_block<T, ADD>(a, acc, parts + wave * store_floats<2>(), row0 + wm * 64, col0 + wn * 64, row0);
 }
 
-// Partial results of the pieces, in their order, to the output.  3 pieces of 517 x 1031, added to: 6 us.
+// Partial results of the pieces, in their order, to the output; a lane has 8 values.  Only results of
+// few tiles are cut, so a launch has a few thousand workgroups at most.  3 pieces of 517 x 1031, added
+// to: 6 us.
 template <typename T, bool ADD>
 __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
   const int chunks = (a.k + 7) / 8;
-  const int64_t total = int64_t(a.n) * chunks;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
-    const int row = int(i / chunks), col = int(i - int64_t(row) * chunks) * 8;
-    T* out = static_cast<T*>(a.out) + int64_t(row) * a.ldo;
-    Eight<T> old;
-    old.clear();
-    if (ADD) old.load(out, col, a.k);
-    float sum[8] = {};
-    for (int s0 = 0; s0 < a.splits; s0 += 4) {  // four pieces' loads in flight
-      Eight<float> v[4];
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= int64_t(a.n) * chunks) return;
+  const int row = int(i / chunks), col = int(i - int64_t(row) * chunks) * 8;
+  T* out = static_cast<T*>(a.out) + int64_t(row) * a.ldo;
+  Eight<T> old;
+  old.clear();
+  if (ADD) old.load(out, col, a.k);
+  float sum[8] = {};
+  for (int s0 = 0; s0 < a.splits; s0 += 4) {  // four pieces' loads in flight
+    Eight<float> v[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        v[s].clear();
-        if (s0 + s < a.splits) v[s].load(a.parts + (int64_t(s0 + s) * a.n + row) * a.k, col, a.k);
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += v[s].get(e);
+    for (int s = 0; s < 4; ++s) {
+      v[s].clear();
+      if (s0 + s < a.splits) v[s].load(a.parts + (int64_t(s0 + s) * a.n + row) * a.k, col, a.k);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = ADD ? old.get(e) + sum[e] : sum[e];
-    Eight<T>::store(out, col, a.k, sum);
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[s].get(e);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = ADD ? old.get(e) + sum[e] : sum[e];
+  Eight<T>::store(out, col, a.k, sum);
 }
 
 template <typename T, bool ADD>
@@ -443,7 +444,7 @@ void launch(const WgradArgs& a, bool dy_bf16, int tile, hipStream_t s) {
 template <typename T, bool ADD>
 void join(const WgradArgs& a, hipStream_t s) {
   const int64_t work = (int64_t(a.n) * ((a.k + 7) / 8) + 255) / 256;
-  hipLaunchKernelGGL((k_wgrad_join<T, ADD>), dim3(uint32_t(work < 65536 ? work : 65536)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_wgrad_join<T, ADD>), dim3(uint32_t(work)), dim3(256), 0, s, a);
 }
 
 }  // namespace
