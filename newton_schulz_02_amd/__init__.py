@@ -1181,25 +1181,25 @@ class Codes:
         return dequantize(self, dtype, out=out, stream=stream)
 
 
-def _linear_device(torch, *operands):
+def _linear_device(torch, first, *others):
     """The one GPU that tensors (or Codes) are on; none of them may need a gradient."""
-    device, tangents = operands[0].device, torch.autograd.forward_ad._current_level >= 0
-    for t in operands:
-        if t is None:
-            continue
-        if t.requires_grad and torch.is_grad_enabled() or tangents and _has_tangent(torch, t):
-            raise ValueError("an operand needs a gradient or has a tangent, and the 8-bit operators record neither: call "
-                             "them from a torch.autograd.Function, or under torch.no_grad() without a tangent")
-        if t.device != device:
-            raise ValueError(f"operands must be on one GPU, not on {device} and {t.device}")
+    device, graph = first.device, first.requires_grad
+    for t in others:
+        if t is not None:
+            graph = graph or t.requires_grad
+            if t.device != device:
+                raise ValueError(f"operands must be on one GPU, not on {device} and {t.device}")
+    if graph and torch.is_grad_enabled() or torch.autograd.forward_ad._current_level >= 0 and _has_tangent(torch, first, *others):
+        raise ValueError("an operand needs a gradient or has a tangent, and the 8-bit operators record neither: call "
+                         "them from a torch.autograd.Function, or under torch.no_grad() without a tangent")
     if device.type != "cuda":
         raise ValueError(f"operands must be on a GPU, not on {device}")
     return device
 
 
-def _has_tangent(torch, t) -> bool:
-    t = t._scale if isinstance(t, Codes) else t
-    return t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None
+def _has_tangent(torch, *operands) -> bool:
+    tensors = [t._scale if isinstance(t, Codes) else t for t in operands]
+    return any(t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _view_arg(name, t):
