@@ -183,6 +183,14 @@ def test_workspace_sizes():
     assert nm.lib().muon_quantize_size(ref(view(4, 8)), 0, None) == nm.MUON_EINVAL
 
 
+@pytest.mark.parametrize("tokens,outputs,ld,inputs,pieces", [(777, 517, 524, 1031, 3), (8192, 768, 768, 768, 7),
+                                                             (512, 768, 768, 768, 1), (4096, 4096, 4096, 4096, 1)])
+def test_pieces_of_a_weight_gradient(tokens, outputs, ld, inputs, pieces):
+    """The plans whose times the cost model's comment gives: each piece has its partial results in the workspace."""
+    rc, n = size_of("muon_weight_grad_size", ref(view(tokens, outputs, ld=ld)), ref(codes(tokens, inputs, block=128)))
+    assert rc == 0 and n == (pieces * outputs * inputs * 4 if pieces > 1 else 0)
+
+
 @pytest.mark.parametrize("call,kind", [
     (lambda x: nm.quantize(x), ValueError),
     (lambda x: nm.Codes.empty(4, 8, device="cpu"), ValueError),
