@@ -7,9 +7,12 @@
 // when step ks begins: the last group of step ks reads the first fragments of the next one, and
 // matrix instructions (v_mfma_i32_32x32x32_i8; the sums are exact) go on over the barrier.
 //
-// 16384 x 11008 x 4096 take 630 to 660 us (2.3 POP/s), 8192^3 445 (2.5): bound by power, at 1.6 GHz with
-// the matrix units busy 64 % of the time.  2048 x 4096 x 4096 take 39 us in 256 x 128 tiles, bound by LDS
-// accesses, of which a tile of half the results needs two thirds.
+// 16384 x 11008 x 4096 take 640 to 690 us by card and by how long it has run (2.1 to 2.3 POP/s), 8192^3 454
+// (2.4): power holds the clock at 1.65 GHz, with the matrix units busy 64 % of the time.
+// 2048 x 4096 x 4096 take 39 to 43 us in 256 x 128 tiles, at 2.36 GHz: the loads decide.  Of the time that the
+// compute units are busy the matrix units are for 37 %, LDS reads take 21 % and the L1 caches wait for
+// L2 60 %: rows of 64 bytes are requests of 64 bytes, about 118 of them in flight for 430 cycles each, so
+// 18 bytes a cycle and compute unit arrive.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -7,7 +7,7 @@
 // tokens as rows, and ds_read_b64_tr_b16 turns them as they are read: of each group of 16 lanes,
 // lane i gives the address of 4 columns of token i / 4, and gets 4 tokens of column i.
 //
-// 16384 tokens x 11008 x 4096 take 1210 to 1260 us (1.2 PFLOP/s): bound by power, at 1.7 GHz with the matrix
+// 16384 tokens x 11008 x 4096 take 1210 to 1275 us by card (1.2 PFLOP/s): bound by power, at 1.7 GHz with the matrix
 // units busy 66 % of the time that the 688 tiles of 256 x 256 take.  In a tile of 128 x 128 a step takes
 // 0.63 us, of which LDS accesses are the most.
 //
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void k_wgrad(WgradArgs a) {
 }
 
 // fp32 dy: 128 x 128 tiles of 4 waves, 32 tokens a step, through registers; two workgroups share a
-// compute unit, so that one multiplies while the other writes to LDS.  4096^3 takes 1173 us (117 TFLOP/s).
+// compute unit, so that one multiplies while the other writes to LDS.  4096^3 takes 1175 us (117 TFLOP/s).
 template <typename T, bool ADD>
 __global__ __launch_bounds__(256, 2) void k_wgrad_f32(WgradArgs a) {
   constexpr int kT = 128, kTok = 32, kLd = kT + 4, kUnits = kTok / 16;
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(256, 2) void k_wgrad_f32(WgradArgs a) {
 
 // Partial results of the pieces, in their order, to the output; a lane has 8 values.  Only results of
 // few tiles are cut, so a launch has a few thousand workgroups at most.  3 pieces of 517 x 1031, added
-// to: 6 us.
+// to: 5.4 us.
 template <typename T, bool ADD>
 __global__ __launch_bounds__(256) void k_wgrad_join(WgradArgs a) {
   const int chunks = (a.k + 7) / 8;

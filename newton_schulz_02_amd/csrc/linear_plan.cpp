@@ -131,8 +131,8 @@ bool quant_too_large(const QuantPlan& p) {
 // Few tiles: the tokens are cut into pieces, whose partial results a second launch joins.  In
 // microseconds: a step of 64 tokens takes 0.63 where each workgroup has a compute unit and 0.8 where
 // some share one (fp32 dy: 4.5, and two share one with little loss); a join takes 1.7, a tenth for each
-// piece and its bytes at 5 TB/s.  (777 tokens, 517 x 1031 results: 17.0 whole, 15.5 in the 3 pieces
-// that this chooses; 8192, 768 x 768: 85.6 whole, 24.3 in 6, 27.6 in 8.)
+// piece and its bytes at 5 TB/s.  (777 tokens, 517 x 1031 results: 17.2 whole, 15.7 in the 3 pieces
+// that this chooses; 8192, 768 x 768: 85.1 whole, 24.8 in 6, 24.1 in the 7 that this chooses, 28.3 in 8.)
 int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
   const double steps = double(ceil_div(a.tokens, 64)), bytes = 8.0 * a.n * a.k;
   auto step = [&](int64_t groups) {
@@ -150,8 +150,8 @@ int32_t wgrad_splits(int64_t tiles, const WgradArgs& a, bool bf16) {
 
 // Which tile: the fewest rounds over the compute units, weighed by what a round takes as a part of a
 // round of 256 x 256 tiles (a smaller tile reads more of its operands for each result).  4096
-// columns summed over: 4096 x 4096 results take 64 us in tiles of 256 x 256 and 76 in 256 x 128,
-// 2048 x 4096 take 42 and 39 (46 in 128 x 128), 512 x 4096 39, 27 and 19.
+// columns summed over, in tiles of 256 x 256, 256 x 128 and 128 x 128: 4096 x 4096 results take 64, 78 and
+// 86 us, 2048 x 4096 take 42, 39 and 42.5, 512 x 4096 37, 24 and 17.3.
 int int8_tile(int64_t rows, int64_t cols) {
   const int64_t full = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 256), kMaxUnits);
   const int64_t half = ceil_div(ceil_div(rows, 256) * ceil_div(cols, 128), kMaxUnits);
@@ -227,6 +227,8 @@ int plan_int8(const muon_codes* a, const muon_view* x, const muon_codes* b, cons
   g.b = static_cast<const int8_t*>(b->q);
   g.b_scale = b->scale;
   p->empty = g.rows == 0 || g.cols == 0;
+  // In the kernel for few rows and in tiles, us: 32 rows of 4096 for 4096 columns 10.6 and 12.8, of 11008 for
+  // 4096 25 and 35.5, of 4096 for 11008 19.4 and 16.6; 64 rows 15.2 and 12.8, 36 and 38, 26 and 17.4.
   p->few = g.rows <= kFewRows;
   p->tile = int8_tile(g.rows, g.cols);
   if (p->few ? g.cols > (1 << 26) : ceil_div(g.rows, 128) * ceil_div(g.cols, 128) > (1 << 23))
@@ -295,6 +297,9 @@ int plan_wgrad(const muon_view* dy, const muon_codes* x, const muon_view* out, i
   if (!p->empty) {
     const int64_t tiles128 = ceil_div(a.n, 128) * ceil_div(a.k, 128), tiles256 = ceil_div(a.n, 256) * ceil_div(a.k, 256);
     if (tiles128 > (1 << 23)) return refuse(err, MUON_EINVAL, "the result is too large");
+    // In tiles of 256 x 256 and of 128 x 128, 4096 tokens added to fp32, us: 192 (4096 x 3000 results) 113 and
+    // 127, 256 (4096 x 4096) 138 and 167, 384 (6144 x 4096) 223 and 238, 688 (11008 x 4096) 353 and 425.  Just
+    // past a round of the compute units the small ones would be faster: 272 (4352 x 4096) 218 and 187.
     if (p->bf16 && tiles256 >= 192) p->tile = kTile256;
     // bf16 rows go to LDS 16 bytes at a time, by 32-bit offsets from the first of 64 tokens.  Others
     // come through registers, in small tiles, or are copied first (517 x 1031 from 777 tokens: 15 us
