@@ -478,6 +478,62 @@ def test_graphs():
             assert torch.equal(few, nm.int8_linear(x[:3], nm.quantize(w)))
 
 
+def test_a_graph_of_named_streams():
+    """A captured layer whose calls name their streams, the weight gradient's one that joins in the
+    capture; replayed on new values, with eager calls between."""
+    x, w, dy = normal(700, 264, BF16, 1), normal(135, 264, BF16, 2), normal(700, 135, BF16, 3)
+    grad = torch.zeros(135, 264, device=DEV)
+    layer_pass(x, w, dy, grad)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        kept = nm.quantize(x, block=True, stream=main)
+        side.wait_stream(main)
+        nm.weight_grad(dy, kept, out=grad, accumulate=True, stream=side)
+        y = nm.int8_linear(x, nm.quantize(w, stream=main), stream=main)
+        dx = nm.int8_linear(dy, nm.quantize(w, transpose=True, stream=main), stream=main)
+        main.wait_stream(side)
+    for turn in range(4):
+        x.copy_(normal(*x.shape, BF16, 40 + turn))
+        dy.copy_(normal(*dy.shape, BF16, 60 + turn))
+        grad.fill_(1.0)
+        graph.replay()
+        other = torch.ones_like(grad)
+        want = layer_pass(x, w, dy, other)
+        torch.cuda.synchronize()
+        assert torch.equal(grad, other) and torch.equal(y, want[0]) and torch.equal(dx, want[1])
+
+
+def test_calls_of_several_threads():
+    """Threads with a stream each: the same results as one after another."""
+    import threading
+
+    data = [(normal(300 + 7 * i, 264, BF16, i), normal(135, 264, BF16, 9), normal(300 + 7 * i, 135, BF16, 30 + i)) for i in range(4)]
+    want = []
+    for x, w, dy in data:
+        grad = torch.zeros(135, 264, device=DEV)
+        want.append((*layer_pass(x, w, dy, grad), grad))
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            x, w, dy = data[i]
+            for _ in range(20):
+                grad = torch.zeros(135, 264, device=DEV)
+                got[i] = (*layer_pass(x, w, dy, grad), grad)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for p, q in zip(want, got):
+        assert q is not None and all(torch.equal(a, b) for a, b in zip(p, q))
+
+
 def test_codes_are_written_in_place():
     x = normal(50, 300, BF16, 1)
     for block in (False, True):
